@@ -142,15 +142,15 @@ def prepare(case, seed):
     slots = torch.randperm(ns, generator=g, device="cuda")[:B].to(torch.int32)
     unit = lambda v: v / v.square().sum(-1, keepdim=True).add(_EPS).sqrt()  # noqa: E731
     slow = lambda *s: torch.exp(rn(*s) * 1.5 - 2.0)  # noqa: E731  decay rates, slow and fast
-    n0 = torch.zeros((ns, hv), dtype=torch.int32, device="cuda")
-    n0[slots.long()] = i32(lens)[:, None].expand(B, hv)
-    # k of a record is that of the key head, once for each value head that reads it
+    n0 = torch.zeros(ns, dtype=torch.int32, device="cuda")
+    n0[slots.long()] = i32(lens)
+    # the key head of each value head
     heads = torch.arange(hv, device="cuda")
     heads = heads % hk if c["tiled"] else heads // (hv // hk)
     s = dict(case=c, lens=lens, heads=heads, cu=i32(cu), slots=slots, accepted=i32(acc),
              state=rn(ns, hv, dk, dv) * 0.05,
              rec_n=n0, rec_e=torch.exp(-slow(ns, hv, D)),
-             rec_k=unit(rn(ns, hk, D, dk))[:, heads].contiguous(), rec_u=rn(ns, hv, D, dv) * 0.5,
+             rec_k=unit(rn(ns, hk, D, dk)), rec_u=rn(ns, hv, D, dv) * 0.5,
              o=torch.zeros((T, hv, dv), dtype=_T[c["out"]], device="cuda"))
     t = _T[c["dtype"]]
     if c["op"] == "draft":
@@ -241,9 +241,10 @@ def _places(s):
 
 
 def _plain_core(s, q, k, v, g, beta):
-    """Commit and draft on padded [seqs, depth, ...] fp32 tensors; q, k per value head."""
+    """Commit and draft on padded [seqs, depth, ...] fp32 tensors."""
+    new_k, q, k = k, q[:, :, s["heads"]], k[:, :, s["heads"]]
     c, slots = s["case"], s["slots"].long()
-    B, D = c["seqs"], c["depth"]
+    D = c["depth"]
     at, there = _places(s)
     j = torch.arange(D, device="cuda")
     # commit: every accepted token's outer product, decayed by the accepted tokens after it
@@ -253,7 +254,7 @@ def _plain_core(s, q, k, v, g, beta):
     after = torch.cat([suffix[:, :, 1:], torch.ones_like(suffix[:, :, :1])], 2)
     ru = torch.where(took[:, None, :, None], s["rec_u"][slots], 0.0) * after[..., None]
     S = s["state"][slots] * suffix[:, :, 0, None, None] + \
-        s["rec_k"][slots].transpose(2, 3) @ ru
+        s["rec_k"][slots][:, s["heads"]].transpose(2, 3) @ ru
     s["state"][slots] = S
     # draft: the token recurrence on a copy of the state that is dropped
     en = torch.where(there[..., None], torch.exp(g), 1.0)
@@ -269,17 +270,16 @@ def _plain_core(s, q, k, v, g, beta):
     # the record's rows of this draft; rows behind its last token stay as they were
     put = lambda name, new, m: s[name].index_put_((slots,), torch.where(m, new, s[name][slots]))  # noqa: E731,E501
     put("rec_e", torch.exp(g).transpose(1, 2), there[:, None])
-    put("rec_k", k.transpose(1, 2), there[:, None, :, None])
+    put("rec_k", new_k.transpose(1, 2), there[:, None, :, None])
     put("rec_u", u.transpose(1, 2), there[:, None, :, None])
-    s["rec_n"][slots] = (s["cu"][1:] - s["cu"][:-1])[:, None].expand(B, c["hv"])
+    s["rec_n"][slots] = s["cu"][1:] - s["cu"][:-1]
     return o[there]                                                      # packed [T, hv, dv]
 
 
 def _plain_draft(s):
     at, _ = _places(s)
     f = lambda t: t.float()[at]  # noqa: E731
-    o = _plain_core(s, f(s["q"])[:, :, s["heads"]], f(s["k"])[:, :, s["heads"]], f(s["v"]),
-                    f(s["g"]), f(s["beta"]))
+    o = _plain_core(s, f(s["q"]), f(s["k"]), f(s["v"]), f(s["g"]), f(s["beta"]))
     return _outputs(s, o.to(_T[s["case"]["out"]]))
 
 
@@ -308,7 +308,7 @@ def _plain_layer(s):
     zz = a + s["dt_bias"]
     g = -torch.exp(s["A_log"]) * (torch.clamp(zz, min=0) + torch.log1p(torch.exp(-zz.abs())))
     beta = 1.0 / (1.0 + torch.exp(-b))
-    o = _plain_core(s, q[:, :, s["heads"]], k[:, :, s["heads"]], v, g[at], beta[at])
+    o = _plain_core(s, q, k, v, g[at], beta[at])
     if c["gate"]:
         z = s["z"].float()
         o = o / torch.sqrt(o.square().mean(-1, keepdim=True) + _EPS) * s["norm_w"] * \
@@ -373,7 +373,8 @@ def exact(case, seed):
         S = out["state"][slot]
         for j in range(acc[n]):  # the accepted tokens, one after another
             S = out["rec_e"][slot, :, j, None, None] * S + \
-                torch.einsum("hd,hc->hdc", out["rec_k"][slot, :, j], out["rec_u"][slot, :, j])
+                torch.einsum("hd,hc->hdc", out["rec_k"][slot, heads, j],
+                             out["rec_u"][slot, :, j])
         out["state"][slot] = S
         T, span = lens[n], slice(t0, t0 + lens[n])
         if c["op"] == "layer":
@@ -406,7 +407,7 @@ def exact(case, seed):
             u = beta[i][:, None] * (v[i] - torch.einsum("hdc,hd->hc", S, ki))
             S = S + torch.einsum("hd,hc->hdc", ki, u)
             o[t0 + i] = torch.einsum("hdc,hd->hc", S, qi)
-            out["rec_e"][slot, :, i], out["rec_k"][slot, :, i] = g[i].exp(), ki
+            out["rec_e"][slot, :, i], out["rec_k"][slot, :, i] = g[i].exp(), k[i]
             out["rec_u"][slot, :, i] = u
         out["rec_n"][slot] = T
         t0 += T
