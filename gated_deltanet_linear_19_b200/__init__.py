@@ -25,7 +25,8 @@ __all__ = ["Dims", "GdnError", "conv_step", "decode_step", "layer_decode",
            "OutGate",
            "decode_workspace_size", "chunked_prefill", "layer_prefill",
            "chunked_prefill_noalloc", "prefill_workspace_size", "state_slot_copy", "device_status", "status_string",
-           "front_outputs", "DTYPE_CODE"]
+           "front_outputs", "DTYPE_CODE", "DraftRecord", "draft_record", "draft_workspace_size",
+           "draft_step", "layer_draft"]
 
 DTYPE_CODE = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16, torch.float16: GDN_F16}
 
@@ -311,6 +312,112 @@ def gated_norm(dims: Dims, o, gate: OutGate, out=None, *, stream=None):
                             _code(out), o.shape[0], _stream(stream))
     _check(rc, "gdn_gated_norm")
     return out
+
+
+@dataclass(frozen=True)
+class DraftRecord:
+    """Per-slot records of drafted tokens (gdn_draft_record), updated in place by the draft
+    steps: n [n_slots] int32, e [n_slots, H_v, depth], k [n_slots, H_k, depth, d_k],
+    u [n_slots, H_v, depth, d_v] fp32, x [n_slots, depth, conv_dim] of the conv state's dtype
+    (layer drafts with a convolution only)."""
+    n: torch.Tensor
+    e: torch.Tensor
+    k: torch.Tensor
+    u: torch.Tensor
+    x: torch.Tensor | None = None
+
+    @property
+    def depth(self) -> int:
+        return self.e.shape[2]
+
+    def _c(self, dims: Dims, conv_dtype=None):
+        s, hk, hv, d = dims.n_slots, dims.H_k, dims.H_v, self.depth
+        if (self.n.shape != (s,) or self.e.shape != (s, hv, d)
+                or self.k.shape != (s, hk, d, dims.d_k) or self.u.shape != (s, hv, d, dims.d_v)
+                or self.n.dtype != torch.int32 or self.e.dtype != torch.float32
+                or self.k.dtype != torch.float32 or self.u.dtype != torch.float32):
+            raise ValueError("gdn: draft record does not fit the dims")
+        if conv_dtype is not None and (self.x is None or self.x.dtype != conv_dtype
+                                       or self.x.shape != (s, d, dims.conv_dim)):
+            raise ValueError("gdn: draft record's x does not fit the dims and conv state")
+        return ctypes.byref(_lib.GdnDraftRecord(
+            d, _p(self.n), _p(self.e), _p(self.k), _p(self.u),
+            _p(self.x) if conv_dtype is not None else None))
+
+
+def draft_record(dims: Dims, depth: int, *, conv_dtype=torch.bfloat16,
+                 device="cuda") -> DraftRecord:
+    """Allocate empty records of up to `depth` tokens (1 to 16) for every slot."""
+    z = lambda *s, dt=torch.float32: torch.zeros(s, dtype=dt, device=device)  # noqa: E731
+    s = dims.n_slots
+    return DraftRecord(z(s, dt=torch.int32), z(s, dims.H_v, depth),
+                       z(s, dims.H_k, depth, dims.d_k), z(s, dims.H_v, depth, dims.d_v),
+                       z(s, depth, dims.conv_dim, dt=conv_dtype) if dims.d_conv > 1 else None)
+
+
+def draft_workspace_size(dims: Dims, T_total: int, n_seqs: int, depth: int) -> int:
+    return int(_lib.load().gdn_draft_workspace_size(ctypes.byref(dims.c()), int(T_total),
+                                                    int(n_seqs), int(depth)))
+
+
+def _draft_seqs(slot_ids, cu_seqlens, accepted, reset):
+    """The number of sequences, after checking the per-sequence arrays against it."""
+    n = slot_ids.numel()
+    if slot_ids.dtype != torch.int32 or \
+            (accepted is not None and (accepted.dtype != torch.int32 or accepted.numel() != n)) or \
+            (cu_seqlens is not None and (cu_seqlens.dtype != torch.int32
+                                         or cu_seqlens.numel() != n + 1)) or \
+            (reset is not None and (reset.element_size() != 1 or reset.numel() != n)):
+        raise ValueError("gdn: slot_ids, accepted [n], cu_seqlens [n + 1] are int32 and reset [n] "
+                         "holds bytes")
+    return n
+
+
+def _draft_ws(lib, cdims, T, n_seqs, depth, workspace, device):
+    if workspace is None:
+        need = int(lib.gdn_draft_workspace_size(cdims, T, n_seqs, depth))
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def draft_step(dims: Dims, q, k, v, g, beta, state, slot_ids, cu_seqlens, accepted,
+               record: DraftRecord, o, *, reset=None, workspace=None, stream=None):
+    """gdn_draft_step: commit the accepted tokens of each slot's record, then run the new drafted
+    tokens without advancing the state (o written, record replaced). cu_seqlens=None: one new
+    token per sequence; accepted=None: nothing is committed. Allocates the workspace if not
+    given."""
+    lib = _lib.load()
+    cdims = ctypes.byref(dims.c())
+    T = q.shape[0]
+    n_seqs = _draft_seqs(slot_ids, cu_seqlens, accepted, reset)
+    ws, ws_bytes = _draft_ws(lib, cdims, T, n_seqs, record.depth, workspace, state.device)
+    rc = lib.gdn_draft_step(cdims, _p(q), _p(k), _p(v), _code(q), _p(g), _p(beta), _p(state),
+                            _p(slot_ids), _p(cu_seqlens), _p(reset), _p(accepted), n_seqs, T,
+                            record._c(dims), _p(o), _code(o), _p(ws), ws_bytes, _stream(stream))
+    _check(rc, "gdn_draft_step")
+
+
+def layer_draft(dims: Dims, x, conv_w, conv_state, cu_seqlens, slot_ids, accepted, a, b, A_log,
+                dt_bias, state, record: DraftRecord, o, *, eps=1e-6, q_scale=None, reset=None,
+                workspace=None, gate=None, stream=None):
+    """gdn_layer_draft: draft_step from raw projections x [T, conv_dim], the convolution's window
+    rolled to the accepted tokens, with the optional OutGate. Allocates the workspace if not
+    given."""
+    lib = _lib.load()
+    if q_scale is None:
+        q_scale = dims.d_k ** -0.5
+    cdims = ctypes.byref(dims.c())
+    T = x.shape[0]
+    n_seqs = _draft_seqs(slot_ids, cu_seqlens, accepted, reset)
+    ws, ws_bytes = _draft_ws(lib, cdims, T, n_seqs, record.depth, workspace, state.device)
+    conv_dtype = conv_state.dtype if conv_state is not None else None
+    rc = lib.gdn_layer_draft(cdims, _p(x), _code(x), _p(conv_w), _p(conv_state),
+                             DTYPE_CODE[conv_dtype] if conv_dtype is not None else GDN_F32,
+                             _p(cu_seqlens), _p(slot_ids), _p(reset), _p(accepted), n_seqs, T,
+                             _p(a), _p(b), _p(A_log), _p(dt_bias), float(eps), float(q_scale),
+                             _p(state), record._c(dims, conv_dtype), _p(o), _code(o), _p(ws),
+                             ws_bytes, _gate(gate), _stream(stream))
+    _check(rc, "gdn_layer_draft")
 
 
 def prefill_workspace_size(dims: Dims, T_total: int, n_seqs: int, chunk: int = 64,

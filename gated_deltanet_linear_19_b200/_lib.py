@@ -40,7 +40,8 @@ EXPORTS = ("gdn_conv_step", "gdn_decode_step", "gdn_layer_decode", "gdn_decode_w
            "gdn_device_status", "gdn_status_string", "gdn_abi_version", "gdn_gated_norm",
            "gdn_debug_set_wait_limit", "gdn_decode_pipe_buffer_size", "gdn_decode_pipe_create",
            "gdn_decode_pipe_step", "gdn_decode_pipe_flush", "gdn_decode_pipe_destroy",
-           "gdn_decode_pipe_packed_bytes", "gdn_decode_pipe_step_packed")
+           "gdn_decode_pipe_packed_bytes", "gdn_decode_pipe_step_packed",
+           "gdn_draft_step", "gdn_layer_draft", "gdn_draft_workspace_size")
 
 
 GDN_LAYOUT_DEFAULT = 0
@@ -57,6 +58,11 @@ class GdnDims(ctypes.Structure):
 class GdnOutGate(ctypes.Structure):
     _fields_ = [("z", ctypes.c_void_p), ("z_dtype", ctypes.c_int32),
                 ("norm_w", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
+class GdnDraftRecord(ctypes.Structure):
+    _fields_ = [("depth", ctypes.c_int32), ("n", ctypes.c_void_p), ("e", ctypes.c_void_p),
+                ("k", ctypes.c_void_p), ("u", ctypes.c_void_p), ("x", ctypes.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -131,6 +137,15 @@ def load(path: str | None = None):
         lib.gdn_decode_pipe_flush.restype = ctypes.c_int
         lib.gdn_decode_pipe_destroy.argtypes = [P]
         lib.gdn_decode_pipe_destroy.restype = ctypes.c_int
+        R = ctypes.POINTER(GdnDraftRecord)
+        lib.gdn_draft_step.argtypes = [D, P, P, P, I32, P, P, P, P, P, P, P, I32, I64, R, P, I32,
+                                       P, S, P]
+        lib.gdn_draft_step.restype = ctypes.c_int
+        lib.gdn_layer_draft.argtypes = [D, P, I32, P, P, I32, P, P, P, P, I32, I64, P, P, P, P, F,
+                                        F, P, R, P, I32, P, S, G, P]
+        lib.gdn_layer_draft.restype = ctypes.c_int
+        lib.gdn_draft_workspace_size.argtypes = [D, I64, I32, I32]
+        lib.gdn_draft_workspace_size.restype = S
         lib.gdn_abi_version.argtypes = []
         lib.gdn_abi_version.restype = I32
         _lib = lib

@@ -481,6 +481,121 @@ int gdn_layer_prefill(const gdn_dims* dims, const void* x, int32_t x_dtype, cons
   return from_cuda(gdn::launch_gated_norm(ga, s));
 }
 
+namespace {
+// The record arrays of a draft step; `need_x`: the layer form with a convolution window.
+int record_check(const gdn_dims* d, const gdn_draft_record* r, bool need_x) {
+  if (d->H_v / d->H_k > 256) return GDN_EUNSUPPORTED;
+  if (!r || r->depth < 1 || r->depth > kShortMax || !r->n || !r->e || !r->k || !r->u)
+    return GDN_EINVAL;
+  if (need_x && !r->x) return GDN_EINVAL;
+  const void* ptrs[] = {r->n, r->e, r->k, r->u, r->x};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return GDN_EALIGN;
+  return GDN_OK;
+}
+size_t draft_ws_bytes(const gdn_dims* d, int64_t T_total, int32_t n_seqs, int32_t depth) {
+  return gdn::draft_workspace(d->H_k, d->H_v, d->d_k, d->d_v, T_total, n_seqs, depth);
+}
+}  // namespace
+
+size_t gdn_draft_workspace_size(const gdn_dims* dims, int64_t T_total, int32_t n_seqs,
+                                int32_t depth) {
+  if (check_dims(dims) != GDN_OK || T_total < 0 || n_seqs <= 0 || depth < 1 || depth > kShortMax)
+    return 0;
+  return draft_ws_bytes(dims, T_total, n_seqs, depth);
+}
+
+int gdn_draft_step(const gdn_dims* dims, const void* q, const void* k, const void* v,
+                   int32_t qkv_dtype, const float* g, const float* beta, float* state,
+                   const int32_t* slot_ids, const int32_t* cu_seqlens, const uint8_t* reset,
+                   const int32_t* accepted, int32_t n_seqs, int64_t T_total,
+                   const gdn_draft_record* record, void* o, int32_t o_dtype, void* workspace,
+                   size_t workspace_bytes, gdn_stream_t stream) {
+  int rc = check_dims(dims);
+  if (rc != GDN_OK) return rc;
+  if (n_seqs < 0 || n_seqs > 65535 || T_total < 0) return GDN_EINVAL;
+  if (n_seqs == 0) return T_total == 0 ? GDN_OK : GDN_EINVAL;
+  if (!qkv_dtype_ok(qkv_dtype) || !io_dtype_ok(o_dtype)) return GDN_EINVAL;
+  if (!state || !slot_ids) return GDN_EINVAL;
+  if (!cu_seqlens && T_total != n_seqs) return GDN_EINVAL;  // NULL: one token per sequence
+  if (T_total > 0 && (!q || !k || !v || !g || !beta || !o)) return GDN_EINVAL;
+  rc = record_check(dims, record, false);
+  if (rc != GDN_OK) return rc;
+  const void* ptrs[] = {q, k, v, g, beta, state, o, workspace};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return GDN_EALIGN;
+  if (!workspace || workspace_bytes < draft_ws_bytes(dims, T_total, n_seqs, record->depth))
+    return GDN_EWORKSPACE;
+  gdn::DraftArgs da{};
+  da.q = q; da.k = k; da.v = v; da.qkv_dtype = qkv_dtype; da.g = g; da.beta = beta;
+  da.state = state; da.slot_ids = slot_ids; da.cu_seqlens = cu_seqlens; da.reset = reset;
+  da.accepted = accepted; da.n_seqs = n_seqs; da.T_total = T_total; da.rec = *record;
+  da.o = o; da.o_dtype = o_dtype; da.workspace = workspace;
+  da.H_k = dims->H_k; da.H_v = dims->H_v; da.d_k = dims->d_k; da.d_v = dims->d_v;
+  da.n_slots = dims->n_slots; da.layout = dims->layout;
+  da.status = status_ptr();
+  if (!da.status) return GDN_ECUDA;
+  return from_cuda(gdn::launch_draft(da, nullptr, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int gdn_layer_draft(const gdn_dims* dims, const void* x, int32_t x_dtype, const float* conv_w,
+                    void* conv_state, int32_t conv_state_dtype, const int32_t* cu_seqlens,
+                    const int32_t* slot_ids, const uint8_t* reset, const int32_t* accepted,
+                    int32_t n_seqs, int64_t T_total, const float* a, const float* b,
+                    const float* A_log, const float* dt_bias, float eps, float q_scale,
+                    float* state, const gdn_draft_record* record, void* o, int32_t o_dtype,
+                    void* workspace, size_t workspace_bytes, const gdn_out_gate* gate,
+                    gdn_stream_t stream) {
+  int rc = check_dims(dims);
+  if (rc != GDN_OK) return rc;
+  if (n_seqs < 0 || n_seqs > 65535 || T_total < 0) return GDN_EINVAL;
+  if (n_seqs == 0) return T_total == 0 ? GDN_OK : GDN_EINVAL;
+  if (!io_dtype_ok(x_dtype) || !io_dtype_ok(o_dtype)) return GDN_EINVAL;
+  const int R = dims->d_conv > 0 ? dims->d_conv - 1 : 0;
+  if (dims->d_conv > 0 && !conv_w) return GDN_EINVAL;
+  if (dims->d_conv == 0 && conv_w) return GDN_EINVAL;
+  if (R > 0) {
+    if (!conv_state || !io_dtype_ok(conv_state_dtype)) return GDN_EINVAL;
+  } else if (conv_state) {
+    return GDN_EINVAL;
+  }
+  if (!state || !slot_ids || !A_log || !dt_bias) return GDN_EINVAL;
+  if (!cu_seqlens && T_total != n_seqs) return GDN_EINVAL;
+  if (T_total > 0 && (!x || !o || !gates_ok(dims, a, b))) return GDN_EINVAL;
+  if (!(eps >= 0.0f)) return GDN_EINVAL;
+  if (T_total > 0) {
+    rc = gate_check(gate);
+    if (rc != GDN_OK) return rc;
+  }
+  rc = record_check(dims, record, R > 0);
+  if (rc != GDN_OK) return rc;
+  const void* ptrs[] = {x, conv_w, conv_state, a, b, A_log, dt_bias, state, o, workspace};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return GDN_EALIGN;
+  if (!workspace || workspace_bytes < draft_ws_bytes(dims, T_total, n_seqs, record->depth))
+    return GDN_EWORKSPACE;
+  gdn::DraftArgs da{};
+  da.x = x ? x : workspace;  // no new tokens: only commits, x is not read
+  da.x_dtype = x_dtype; da.conv_w = conv_w;
+  da.conv_state = conv_state; da.conv_state_dtype = R > 0 ? conv_state_dtype : GDN_F32;
+  da.fa = a; da.fb = b; da.A_log = A_log; da.dt_bias = dt_bias; da.eps = eps;
+  da.q_scale = q_scale;
+  da.state = state; da.slot_ids = slot_ids; da.cu_seqlens = cu_seqlens; da.reset = reset;
+  da.accepted = accepted; da.n_seqs = n_seqs; da.T_total = T_total; da.rec = *record;
+  da.o = o; da.o_dtype = o_dtype; da.workspace = workspace;
+  da.H_k = dims->H_k; da.H_v = dims->H_v; da.d_k = dims->d_k; da.d_v = dims->d_v;
+  da.d_conv = dims->d_conv; da.n_slots = dims->n_slots; da.layout = dims->layout;
+  da.status = status_ptr();
+  if (!da.status) return GDN_ECUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  gdn::GateArgs ga{};
+  if (gate) {
+    ga.z = gate->z; ga.z_dtype = gate->z_dtype; ga.norm_w = gate->norm_w; ga.eps = gate->eps;
+    ga.out = o; ga.out_dtype = o_dtype;
+  }
+  return from_cuda(gdn::launch_draft(da, gate ? &ga : nullptr, s));
+}
+
 int gdn_gated_norm(const gdn_dims* dims, const void* o, int32_t o_dtype, const gdn_out_gate* gate,
                    void* out, int32_t out_dtype, int64_t T_total, gdn_stream_t stream) {
   int rc = check_dims(dims);

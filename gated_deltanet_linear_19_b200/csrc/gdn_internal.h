@@ -81,6 +81,30 @@ struct PrefillArgs {
   float eps, q_scale;
 };
 
+// The draft step (gdn_draft_step, gdn_layer_draft): with x set, q, k, v, g, beta are computed
+// from it (v into the workspace), else they are given.
+struct DraftArgs {
+  const void* q; const void* k; const void* v; int qkv_dtype;
+  const float* g; const float* beta;
+  const void* x; int x_dtype;
+  const float* conv_w;
+  void* conv_state; int conv_state_dtype;
+  const float* fa; const float* fb; const float* A_log; const float* dt_bias;
+  float eps, q_scale;
+  float* state; const int32_t* slot_ids; const int32_t* cu_seqlens; const uint8_t* reset;
+  const int32_t* accepted;
+  int n_seqs; int64_t T_total;
+  gdn_draft_record rec;
+  void* o; int o_dtype;
+  void* workspace;
+  int H_k, H_v, d_k, d_v, d_conv, n_slots;
+  int layout;
+  int32_t* status;
+  // set by the launcher: byte offsets of the workspace's parts, L2 prefetch distance in blocks
+  size_t ws_hdr, ws_qk, ws_rk, ws_coef, ws_v;
+  int pf_dist;
+};
+
 struct SlotCopyArgs {
   float* state; void* conv_state; int conv_state_dtype;
   const int32_t* src; const int32_t* dst; int n;
@@ -110,6 +134,9 @@ cudaError_t launch_recurrent(const PrefillArgs& a, int max_len, cudaStream_t s);
 // front computed inside; d_k = d_v = 128 and H_v = H_k or 2 H_k (else cudaErrorNotSupported).
 bool layer_short_supported(const PrefillArgs& a);
 cudaError_t launch_layer_short(const PrefillArgs& a, int max_len, cudaStream_t s);
+size_t draft_workspace(int H_k, int H_v, int d_k, int d_v, int64_t T_total, int n_seqs, int depth);
+// gate: nullptr, or the output gate's z, norm_w, eps and out (its o lies in the workspace)
+cudaError_t launch_draft(const DraftArgs& a, const GateArgs* gate, cudaStream_t s);
 cudaError_t launch_slot_copy(const SlotCopyArgs& a, cudaStream_t s);
 cudaError_t launch_gated_norm(const GateArgs& a, cudaStream_t s);
 

@@ -15,8 +15,9 @@ from __future__ import annotations
 import torch
 
 from . import (DecodePipe, GDN_PREFILL_OUT_GATE, GDN_PREFILL_RECURRENT, GDN_PREFILL_SIMT, Dims,
-               chunked_prefill, conv_step, decode_workspace_size, front_outputs, gated_norm,
-               layer_decode, layer_decode_plan, layer_prefill, prefill_workspace_size)
+               chunked_prefill, conv_step, decode_workspace_size, draft_record,
+               draft_workspace_size, front_outputs, gated_norm, layer_decode, layer_decode_plan,
+               layer_draft, layer_prefill, prefill_workspace_size)
 
 
 class GDNLayer:
@@ -99,6 +100,42 @@ class GDNLayer:
         return DecodePipe(self.dims, n_seqs, self.conv_w, self.conv_state, self.A_log,
                           self.dt_bias, self.state, x_dtype=x_dtype, o_dtype=self.o_dtype,
                           eps=self.eps, q_scale=self.q_scale, stream=stream)
+
+    # ------------------------------------------------------------------ drafts with rollback
+    def draft_record(self, depth: int):
+        """Empty draft records of up to `depth` tokens (1 to 16) for every slot of this layer."""
+        dt = self.conv_state.dtype if self.conv_state is not None else torch.bfloat16
+        return draft_record(self.dims, depth, conv_dtype=dt, device=self.device)
+
+    def _draft_ws(self, T: int, n_seqs: int, depth: int):
+        need = draft_workspace_size(self.dims, T, n_seqs, depth)
+        ws = self._bufs.get("draft_ws")
+        if ws is None or ws.numel() < need:
+            ws = torch.empty(max(need, 1), dtype=torch.uint8, device=self.device)
+            self._bufs["draft_ws"] = ws
+        return ws
+
+    def draft(self, x, a, b, cu_seqlens, slot_ids, accepted, record, *, reset=None, out=None,
+              gate=None):
+        """One speculative step: commit the first accepted[n] tokens of each slot's record to its
+        state and convolution window, then run the packed new tokens (x [T, conv_dim], a, b) from
+        there without advancing either -> o [T, H_v, d_v]; the record now holds them."""
+        T = x.shape[0]
+        o = out if out is not None else self._out(T)
+        layer_draft(self.dims, x, self.conv_w, self.conv_state, cu_seqlens, slot_ids, accepted, a,
+                    b, self.A_log, self.dt_bias, self.state, record, o, eps=self.eps,
+                    q_scale=self.q_scale, reset=reset, gate=gate,
+                    workspace=self._draft_ws(T, slot_ids.numel(), record.depth))
+        return o
+
+    def commit_draft(self, slot_ids, accepted, record):
+        """Commit the first accepted[n] recorded tokens of each slot and empty its record (before
+        any other call on those slots, or when a sequence ends)."""
+        d, n = self.dims, slot_ids.numel()
+        none = torch.empty((0, d.conv_dim), dtype=torch.bfloat16, device=self.device)
+        cu = torch.zeros(n + 1, dtype=torch.int32, device=self.device)
+        self.draft(none, None, None, cu, slot_ids, accepted, record,
+                   out=torch.empty((0, d.H_v, d.d_v), dtype=self.o_dtype, device=self.device))
 
     def fused_prefill_applies(self, x, chunk=64, flags=0, qkv_dtype=None) -> bool:
         d = self.dims

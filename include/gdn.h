@@ -304,6 +304,89 @@ int gdn_layer_prefill(const gdn_dims* dims, const void* x, int32_t x_dtype, cons
                       uint32_t flags, const gdn_out_gate* gate, gdn_stream_t stream);
 
 /*
+ * Draft steps with rollback (speculative decoding). Each sequence runs a few drafted tokens from
+ * its COMMITTED state without advancing it; the caller decides how many of them it keeps, and
+ * the next step commits exactly those before it runs its own tokens. One step reads a sequence's
+ * state once and writes it at most once (not at all when nothing is committed); nothing is
+ * copied and nothing is run twice.
+ *
+ * What a commit needs of the drafted tokens lies in caller-owned per-slot record arrays, which
+ * the library reads and writes in place. For a record of n tokens, per value head with
+ * u_j = beta_j (v_j - S_j^T k_j) of the token recurrence (S_j decayed, before token j's update),
+ * committing the first a <= n of them is S <- e_j S + k_j u_j^T for j = 0..a-1.
+ * A record holds its slot's last draft until the slot's next draft step replaces it; accepted = 0
+ * drops it, and so does reset. Every other call (gdn_decode_step, gdn_layer_prefill, ...) works on
+ * the committed state and knows nothing of records: commit first, with a draft step of no new
+ * tokens, then drop the record. gdn_state_slot_copy copies the committed state only.
+ * Zero-filled arrays are empty records.
+ */
+typedef struct gdn_draft_record {
+  int32_t depth; /* tokens a record has room for, 1..16 */
+  int32_t* n;    /* [n_slots] tokens recorded */
+  float* e;      /* [n_slots][H_v][depth] decays exp(g) */
+  float* k;      /* [n_slots][H_k][depth][d_k] keys */
+  float* u;      /* [n_slots][H_v][depth][d_v] */
+  void* x;       /* [n_slots][depth][conv_dim] of conv_state_dtype, raw projections: used by
+                    gdn_layer_draft when d_conv > 1, else NULL */
+} gdn_draft_record;
+
+/*
+ * gdn_draft_step -- one draft step from given q, k, v, g, beta (gdn_conv_step's outputs).
+ * Pages: the per-token step of qwen3next.cpp build_delta_net_autoregressive; the pages have no
+ * rollback.
+ * Sequence n commits the first accepted[n] tokens of its slot's record to state[slot_ids[n]],
+ * then runs its cu_seqlens[n+1] - cu_seqlens[n] new tokens (0 to depth) from that state, writes
+ * their outputs to o and makes them the slot's record (rows behind the last token keep their
+ * values). A sequence with no new tokens only commits. The arithmetic is fp32; o and the record
+ * equal the token recurrence up to fp32 rounding (o rounded once to o_dtype).
+ *   q, k [T_total][H_k][d_k], v [T_total][H_v][d_v] (qkv_dtype F32, F16 or BF16), g, beta
+ *       [T_total][H_v] fp32, g of any size (-inf clears the past)
+ *   state, slot_ids, reset: as gdn_decode_step (reset[n] != 0: zero state, the record is dropped
+ *       and accepted[n] ignored)
+ *   cu_seqlens [n_seqs+1] int32, or NULL when every sequence has one new token (T_total must
+ *       equal n_seqs)
+ *   accepted [n_seqs] int32, or NULL meaning all zero
+ *   o [T_total][H_v][d_v], o_dtype F32 or BF16
+ *   workspace: at least gdn_draft_workspace_size() bytes, 16-byte aligned, overwritten
+ * A sequence with more than depth new tokens, with accepted[n] negative or above the record's
+ * count, or with a bad or repeated slot id is skipped as a whole (state, record and outputs
+ * untouched) and GDN_EINVAL or GDN_ESLOT is recorded. H_v / H_k at most 256
+ * (GDN_EUNSUPPORTED).
+ */
+int gdn_draft_step(const gdn_dims* dims, const void* q, const void* k, const void* v,
+                   int32_t qkv_dtype, const float* g, const float* beta, float* state,
+                   const int32_t* slot_ids, const int32_t* cu_seqlens, const uint8_t* reset,
+                   const int32_t* accepted, int32_t n_seqs, int64_t T_total,
+                   const gdn_draft_record* record, void* o, int32_t o_dtype, void* workspace,
+                   size_t workspace_bytes, gdn_stream_t stream);
+
+/*
+ * gdn_layer_draft -- one draft step of the whole layer from raw projections: the front
+ * (gdn_conv_step, fp32 q, k, v) with the convolution's window behind the accepted tokens, the
+ * draft step, and the optional output gate.
+ * conv_state[slot] is the window behind the committed tokens: it becomes the last d_conv - 1 rows
+ * of [conv_state; the record's first accepted[n] inputs], bit-exactly, and the new tokens' inputs
+ * go to the record.
+ *   x [T_total][conv_dim], conv_w, conv_state, a, b, A_log, dt_bias, eps, q_scale: as
+ *       gdn_conv_step; the other arguments as gdn_draft_step
+ *   gate: NULL, or the output gate (z [T_total][H_v][d_v]); the step then writes fp32 o into the
+ *       workspace and one more kernel gates it into o (rounded once)
+ */
+int gdn_layer_draft(const gdn_dims* dims, const void* x, int32_t x_dtype, const float* conv_w,
+                    void* conv_state, int32_t conv_state_dtype, const int32_t* cu_seqlens,
+                    const int32_t* slot_ids, const uint8_t* reset, const int32_t* accepted,
+                    int32_t n_seqs, int64_t T_total, const float* a, const float* b,
+                    const float* A_log, const float* dt_bias, float eps, float q_scale,
+                    float* state, const gdn_draft_record* record, void* o, int32_t o_dtype,
+                    void* workspace, size_t workspace_bytes, const gdn_out_gate* gate,
+                    gdn_stream_t stream);
+
+/* Workspace bytes of gdn_draft_step and gdn_layer_draft for n_seqs sequences of T_total new
+ * tokens and records of `depth` tokens (0 for invalid arguments). */
+size_t gdn_draft_workspace_size(const gdn_dims* dims, int64_t T_total, int32_t n_seqs,
+                                int32_t depth);
+
+/*
  * gdn_gated_norm -- the output gate on its own: out = RMSNorm(o) * norm_w * SiLU(z) for
  * T_total tokens (see gdn_out_gate), e.g. after gdn_chunked_prefill or gdn_decode_step.
  *   o [T_total][H_v][d_v] (o_dtype F32 or BF16); out likewise (out_dtype F32 or BF16); out
