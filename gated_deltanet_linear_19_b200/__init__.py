@@ -13,7 +13,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import (GDN_BF16, GDN_EALIGN, GDN_ECUDA, GDN_EINVAL, GDN_ESLOT, GDN_ETIMEOUT,
+from ._lib import (GDN_ACT_GELU, GDN_ACT_NONE, GDN_ACT_SIGMOID, GDN_ACT_SILU, GDN_BF16, GDN_EALIGN, GDN_ECUDA, GDN_EINVAL, GDN_ESLOT, GDN_ETIMEOUT,
                    GDN_EUNSUPPORTED, GDN_EWORKSPACE, GDN_F16, GDN_F32, GDN_GATES_MIXED_BA,
                    GDN_GQA_TILED, GDN_LAYOUT_DEFAULT, GDN_OK,
                    GDN_PREFILL_DEFAULT, GDN_PREFILL_OUT_GATE, GDN_PREFILL_RECURRENT,
@@ -26,8 +26,10 @@ __all__ = ["Dims", "GdnError", "conv_step", "decode_step", "layer_decode",
            "decode_workspace_size", "chunked_prefill", "layer_prefill",
            "chunked_prefill_noalloc", "prefill_workspace_size", "state_slot_copy", "device_status", "status_string",
            "front_outputs", "DTYPE_CODE", "DraftRecord", "draft_record", "draft_workspace_size",
-           "draft_step", "layer_draft"]
+           "draft_step", "layer_draft", "linear"]
 
+_ACT = {"none": GDN_ACT_NONE, "silu": GDN_ACT_SILU, "gelu": GDN_ACT_GELU,
+        "sigmoid": GDN_ACT_SIGMOID}
 DTYPE_CODE = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16, torch.float16: GDN_F16}
 
 
@@ -312,6 +314,58 @@ def gated_norm(dims: Dims, o, gate: OutGate, out=None, *, stream=None):
                             _code(out), o.shape[0], _stream(stream))
     _check(rc, "gdn_gated_norm")
     return out
+
+
+def linear(x, w, *, bias=None, act="none", residual=None, out=None, out_dtype=None, stream=None):
+    """gdn_linear: out = act(x w^T + bias) + residual. x [M, K] and w [N, K] bf16 or fp16 with
+    contiguous rows (any row stride that is a multiple of 8 elements), bias [N] fp32, act "none",
+    "silu", "gelu" or "sigmoid", residual and out [M, N] with contiguous rows (out may be the
+    residual). out is allocated (of out_dtype, x's type by default) if not given."""
+    lib = _lib.load()
+    M, K = x.shape
+    N = w.shape[0]
+    dev = x.device
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype or x.dtype, device=dev)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError("gdn: out is not of out_dtype")
+    if not x.is_cuda or w.device != dev or out.device != dev or w.dtype != x.dtype or \
+            w.shape[1] != K or out.shape != (M, N):
+        raise ValueError("gdn: linear takes x [M, K], w [N, K] of one type and out [M, N] on one "
+                         "CUDA device")
+    b = r = None
+    r_code = GDN_F32
+    ldr = N
+    if bias is not None:
+        if bias.shape != (N,) or bias.dtype != torch.float32 or bias.device != dev or \
+                not bias.is_contiguous():
+            raise ValueError("gdn: bias is a contiguous fp32 [N]")
+        b = bias.data_ptr()
+    if residual is not None:
+        if residual.shape != (M, N) or residual.device != dev:
+            raise ValueError("gdn: residual is [M, N]")
+        r, r_code, ldr = residual.data_ptr(), DTYPE_CODE[residual.dtype], _row_stride(residual)
+    args = (x.data_ptr(), _row_stride(x), w.data_ptr(), _row_stride(w), DTYPE_CODE[x.dtype], b,
+            _ACT[act], r, r_code, ldr, out.data_ptr(), DTYPE_CODE[out.dtype], _row_stride(out), M,
+            N, K)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if dev.index == torch.cuda.current_device():
+        rc = lib.gdn_linear(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = lib.gdn_linear(*args, stream.cuda_stream)
+    _check(rc, "gdn_linear")
+    return out
+
+
+def _row_stride(t):
+    """Elements between the rows of a 2-D tensor whose rows are contiguous."""
+    rows, cols = t.shape
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1:
+        raise ValueError("gdn: rows must be contiguous")
+    return s0 if rows > 1 else (cols + 7) // 8 * 8
 
 
 @dataclass(frozen=True)

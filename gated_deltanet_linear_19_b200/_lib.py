@@ -41,12 +41,18 @@ EXPORTS = ("gdn_conv_step", "gdn_decode_step", "gdn_layer_decode", "gdn_decode_w
            "gdn_debug_set_wait_limit", "gdn_decode_pipe_buffer_size", "gdn_decode_pipe_create",
            "gdn_decode_pipe_step", "gdn_decode_pipe_flush", "gdn_decode_pipe_destroy",
            "gdn_decode_pipe_packed_bytes", "gdn_decode_pipe_step_packed",
-           "gdn_draft_step", "gdn_layer_draft", "gdn_draft_workspace_size")
+           "gdn_draft_step", "gdn_layer_draft", "gdn_draft_workspace_size", "gdn_linear")
 
 
 GDN_LAYOUT_DEFAULT = 0
 GDN_GQA_TILED = 1
 GDN_GATES_MIXED_BA = 2
+
+
+GDN_ACT_NONE = 0
+GDN_ACT_SILU = 1
+GDN_ACT_GELU = 2
+GDN_ACT_SIGMOID = 3
 
 
 class GdnDims(ctypes.Structure):
@@ -146,6 +152,9 @@ def load(path: str | None = None):
         lib.gdn_layer_draft.restype = ctypes.c_int
         lib.gdn_draft_workspace_size.argtypes = [D, I64, I32, I32]
         lib.gdn_draft_workspace_size.restype = S
+        lib.gdn_linear.argtypes = [P, I64, P, I64, I32, P, I32, P, I32, I64, P, I32, I64, I64, I32,
+                                   I32, P]
+        lib.gdn_linear.restype = ctypes.c_int
         lib.gdn_abi_version.argtypes = []
         lib.gdn_abi_version.restype = I32
         _lib = lib

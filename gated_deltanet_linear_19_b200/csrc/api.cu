@@ -614,6 +614,34 @@ int gdn_gated_norm(const gdn_dims* dims, const void* o, int32_t o_dtype, const g
   return from_cuda(gdn::launch_gated_norm(ga, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+int gdn_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, int32_t dtype,
+               const float* bias, int32_t act, const void* residual, int32_t residual_dtype,
+               int64_t ldr, void* out, int32_t out_dtype, int64_t ldo, int64_t M, int32_t N,
+               int32_t K, gdn_stream_t stream) {
+  if (dtype != GDN_BF16 && dtype != GDN_F16) return GDN_EINVAL;
+  if (!qkv_dtype_ok(out_dtype) || act < GDN_ACT_NONE || act > GDN_ACT_SIGMOID) return GDN_EINVAL;
+  if (M < 0 || M > 0x7fffffff || N < 1 || K < 8 || K % 8 != 0) return GDN_EINVAL;
+  if (ldx < K || ldw < K || ldx % 8 != 0 || ldw % 8 != 0 || ldo < N) return GDN_EINVAL;
+  if (ldx >= (1LL << 38) || ldw >= (1LL << 38)) return GDN_EINVAL;  // tensor-map stride limit
+  if (residual && (!qkv_dtype_ok(residual_dtype) || ldr < N)) return GDN_EINVAL;
+  if (M == 0) return GDN_OK;
+  if (!x || !w || !out) return GDN_EINVAL;
+  if (!aligned16(x) || !aligned16(w)) return GDN_EALIGN;
+  auto misaligned = [](const void* p, size_t es) {
+    return (reinterpret_cast<uintptr_t>(p) & (es - 1)) != 0;
+  };
+  if (misaligned(out, dtype_size(out_dtype)) || misaligned(bias, 4) ||
+      (residual && misaligned(residual, dtype_size(residual_dtype))))
+    return GDN_EALIGN;
+  gdn::LinearArgs la{};
+  la.x = x; la.ldx = ldx; la.w = w; la.ldw = ldw; la.dtype = dtype; la.bias = bias; la.act = act;
+  la.residual = residual; la.res_dtype = residual_dtype; la.ldr = ldr;
+  la.out = out; la.out_dtype = out_dtype; la.ldo = ldo; la.M = M; la.N = N; la.K = K;
+  la.status = status_ptr();
+  if (!la.status) return GDN_ECUDA;
+  return from_cuda(gdn::launch_linear(la, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 int gdn_chunked_prefill_noalloc(const gdn_dims* dims, const void* q, const void* k,
                                 const void* v, int32_t qkv_dtype, const float* g,
                                 const float* beta, float* state, const int32_t* slot_ids,

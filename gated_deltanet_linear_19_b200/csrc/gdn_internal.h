@@ -105,6 +105,16 @@ struct DraftArgs {
   int pf_dist;
 };
 
+// out[m][n] = act(sum_k x[m][k] w[n][k] + bias[n]) + residual[m][n]; strides in elements.
+struct LinearArgs {
+  const void* x; const void* w; int dtype; int64_t ldx, ldw;
+  const float* bias; int act;
+  const void* residual; int res_dtype; int64_t ldr;
+  void* out; int out_dtype; int64_t ldo;
+  int64_t M; int N, K;
+  int32_t* status;
+};
+
 struct SlotCopyArgs {
   float* state; void* conv_state; int conv_state_dtype;
   const int32_t* src; const int32_t* dst; int n;
@@ -137,6 +147,7 @@ cudaError_t launch_layer_short(const PrefillArgs& a, int max_len, cudaStream_t s
 size_t draft_workspace(int H_k, int H_v, int d_k, int d_v, int64_t T_total, int n_seqs, int depth);
 // gate: nullptr, or the output gate's z, norm_w, eps and out (its o lies in the workspace)
 cudaError_t launch_draft(const DraftArgs& a, const GateArgs* gate, cudaStream_t s);
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
 cudaError_t launch_slot_copy(const SlotCopyArgs& a, cudaStream_t s);
 cudaError_t launch_gated_norm(const GateArgs& a, cudaStream_t s);
 

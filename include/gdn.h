@@ -395,6 +395,32 @@ size_t gdn_draft_workspace_size(const gdn_dims* dims, int64_t T_total, int32_t n
 int gdn_gated_norm(const gdn_dims* dims, const void* o, int32_t o_dtype, const gdn_out_gate* gate,
                    void* out, int32_t out_dtype, int64_t T_total, gdn_stream_t stream);
 
+/* Activations of gdn_linear. GELU is the exact one, x Phi(x). */
+enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1, GDN_ACT_GELU = 2, GDN_ACT_SIGMOID = 3 };
+
+/*
+ * gdn_linear -- out[m][n] = act(sum_k x[m][k] w[n][k] + bias[n]) + residual[m][n]: the projections
+ * around the layer (hidden state to x, z, a and b; the gated output back to the residual stream),
+ * from one token to long prompts.
+ * Pages: ik_llama.cpp src/llama-delta-net.cpp build_layer_attn_linear (the qkvz and beta/alpha
+ * projections, the output projection and the residual sum).
+ * Products are accumulated in fp32 on the tensor cores; bias, activation and residual are applied
+ * in fp32 and the result is rounded once.
+ *   x [M] rows of K elements, ldx elements apart; w [N] rows of K elements, ldw apart; both of
+ *       `dtype`, GDN_BF16 or GDN_F16
+ *   bias [N] fp32 or NULL; act GDN_ACT_*
+ *   residual [M] rows of N elements, ldr apart, residual_dtype F32, BF16 or F16; or NULL
+ *   out [M] rows of N elements, ldo apart, out_dtype F32, BF16 or F16; out may be the residual
+ *       (same address, stride and type), and must not overlap x, w or bias otherwise
+ *   M >= 0, N >= 1 (any value), K >= 8 and a multiple of 8, ldx and ldw multiples of 8 and at least
+ *       K, ldr and ldo at least N (GDN_EINVAL otherwise). x and w are 16-byte aligned
+ *       (GDN_EALIGN); bias, residual and out need only their elements' alignment.
+ */
+int gdn_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, int32_t dtype,
+               const float* bias, int32_t act, const void* residual, int32_t residual_dtype,
+               int64_t ldr, void* out, int32_t out_dtype, int64_t ldo, int64_t M, int32_t N,
+               int32_t K, gdn_stream_t stream);
+
 /*
  * gdn_chunked_prefill_noalloc -- gdn_chunked_prefill on the tensor-core path for callers that
  * cannot allocate device memory for a workspace: for example code that runs inside a host
