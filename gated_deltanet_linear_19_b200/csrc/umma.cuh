@@ -87,6 +87,16 @@ __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// True in one lane of a converged warp. Single-thread tensor-core and copy instructions under
+// this predicate compile to straight uniform-register code; under `lane == 0` every issue carries
+// a loop over the possibly active lanes (measured: 150 against 20 cycles per tcgen05.mma).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+               : "=r"(e));
+  return e != 0;
+}
+
 // ---------------------------------------------------------------- TMEM
 // Whole warp: allocate `ncols` (power of two >= 32) TMEM columns; address written to smem.
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t ncols) {
