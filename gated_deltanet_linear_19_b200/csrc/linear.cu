@@ -18,7 +18,6 @@
 #include <cuda.h>
 
 #include <mutex>
-#include <type_traits>
 
 #include "gdn_common.cuh"
 #include "gdn_internal.h"
@@ -46,9 +45,9 @@ struct LinearKernelArgs {
 };
 
 // ---------------------------------------------------------------- epilogue
-// Activation, residual type and output type are template arguments of the row loops, chosen once
-// per CTA: the loop that runs is a few dozen instructions (with the choices inside it, a tile's
-// epilogue cost 8,000 to 45,000 cycles, most of them instruction fetch).
+// The activation is a template argument of the kernels and the types are chosen once per 4 values,
+// so that the loop that runs is short: as one unrolled body of every variant, instruction fetch
+// alone cost 8,000 to 45,000 cycles per tile.
 template <int ACT>
 __device__ __forceinline__ float activate(float v) {
   if constexpr (ACT == GDN_ACT_SILU) return silu_exact(v);
@@ -56,84 +55,111 @@ __device__ __forceinline__ float activate(float v) {
   if constexpr (ACT == GDN_ACT_SIGMOID) return sigmoidf_(v);
   return v;
 }
-struct NoResidual {};
+__device__ __forceinline__ void store4_as(void* base, int dtype, int64_t i, float4 v) {
+  if (dtype == GDN_BF16) st4(static_cast<__nv_bfloat16*>(base) + i, v);
+  else if (dtype == GDN_F32) st4(static_cast<float*>(base) + i, v);
+  else st4(static_cast<__half*>(base) + i, v);
+}
+__device__ __forceinline__ void store1_as(void* base, int dtype, int64_t i, float v) {
+  if (dtype == GDN_BF16) st(static_cast<__nv_bfloat16*>(base) + i, v);
+  else if (dtype == GDN_F32) st(static_cast<float*>(base) + i, v);
+  else st(static_cast<__half*>(base) + i, v);
+}
 
-// Rows r0, r0 + step, .. below `cnt` of a tile whose row 0 is output row m: 4 columns n .. n + 3 of
-// each, from sums(row) -> float4. Four rows at a time, their residuals loaded together.
-template <int ACT, typename TR, typename TO, typename Sums>
-__device__ __forceinline__ void finish_rows(const LinearKernelArgs& p, int64_t m, int n, int r0,
-                                            int step, int cnt, Sums sums) {
-  if (n >= p.N) return;
-  const int cols = p.N - n < 4 ? p.N - n : 4;
-  float bias[4];
+// Residuals are fetched as raw bits, all loads of a batch before the first use, and ahead of the
+// sums that they are added to.
+constexpr int EP_ROWS = 8;  // rows of a batch of 4-column vectors
+struct ResBatch { uint32_t w[EP_ROWS][4]; };
+__device__ __forceinline__ void fetch_rows(const LinearKernelArgs& p, ResBatch& b, int64_t m, int n,
+                                           int r0, int step, int cnt) {
+  if (p.res_dtype < 0 || !p.vec || n + 4 > p.N) return;
+  const int64_t i0 = (m + r0) * p.ldr + n, is = p.ldr * step;
+  if (p.res_dtype == GDN_F32) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) bias[i] = p.bias && i < cols ? p.bias[n + i] : 0.f;
-  TO* o = static_cast<TO*>(p.out) + (m + r0) * p.ldo + n;
-  const int64_t ostep = p.ldo * step, rstep = p.ldr * step;
-  if (p.vec && cols == 4) {
-    const TR* res = nullptr;
-    if constexpr (!std::is_same<TR, NoResidual>::value)
-      res = static_cast<const TR*>(p.residual) + (m + r0) * p.ldr + n;
-#pragma unroll 1
-    for (int r = r0; r < cnt; r += 4 * step) {
-      float4 x[4], y[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r + i * step < cnt) {
-          if constexpr (!std::is_same<TR, NoResidual>::value) y[i] = ld4(res + i * rstep);
-          x[i] = sums(r + i * step);
-        }
+    for (int i = 0; i < EP_ROWS; ++i)
+      if (r0 + i * step < cnt) {
+        const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const float*>(p.residual) + i0 +
+                                                        i * is);
+        b.w[i][0] = v.x; b.w[i][1] = v.y; b.w[i][2] = v.z; b.w[i][3] = v.w;
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (r + i * step < cnt)
-          st4(o + i * ostep, make_float4(activate<ACT>(x[i].x + bias[0]) + y[i].x,
-                                         activate<ACT>(x[i].y + bias[1]) + y[i].y,
-                                         activate<ACT>(x[i].z + bias[2]) + y[i].z,
-                                         activate<ACT>(x[i].w + bias[3]) + y[i].w));
-      o += 4 * ostep;
-      res += 4 * rstep;
-    }
   } else {
-    // odd strides, and the last columns of an N that is no multiple of 4
-#pragma unroll 1
-    for (int r = r0; r < cnt; r += step, o += ostep) {
-      const float4 x4 = sums(r);
-      const float x[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i >= cols) break;
-        float v = activate<ACT>(x[i] + bias[i]);
-        if constexpr (!std::is_same<TR, NoResidual>::value)
-          v += ld(static_cast<const TR*>(p.residual) + (m + r) * p.ldr + n + i);
-        st(o + i, v);
+    for (int i = 0; i < EP_ROWS; ++i)
+      if (r0 + i * step < cnt) {
+        const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.residual) +
+                                                        i0 + i * is);
+        b.w[i][0] = v.x; b.w[i][1] = v.y;
       }
+  }
+}
+__device__ __forceinline__ float4 residual_of(const uint32_t (&w)[4], int dtype) {
+  if (dtype == GDN_F32)
+    return make_float4(__uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2]),
+                       __uint_as_float(w[3]));
+  if (dtype == GDN_BF16)  // a bf16 is the upper half of the fp32 with the same bits
+    return make_float4(__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xffff0000u),
+                       __uint_as_float(w[1] << 16), __uint_as_float(w[1] & 0xffff0000u));
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w[0]));
+  const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&w[1]));
+  return make_float4(a.x, a.y, c.x, c.y);
+}
+// Rows r0, r0 + step, .. (EP_ROWS of them, below cnt) of a tile whose row 0 is output row m, the 4
+// columns n .. n + 3 of each, from sums(row) -> float4.
+template <int ACT, typename Sums>
+__device__ __forceinline__ void finish_rows(const LinearKernelArgs& p, const ResBatch& b, int64_t m,
+                                            int n, int r0, int step, int cnt, float4 bias,
+                                            Sums sums) {
+  const int64_t i0 = (m + r0) * p.ldo + n, is = p.ldo * step;
+#pragma unroll
+  for (int i = 0; i < EP_ROWS; ++i) {
+    if (r0 + i * step >= cnt) break;
+    const float4 x = sums(r0 + i * step);
+    float4 y = make_float4(activate<ACT>(x.x + bias.x), activate<ACT>(x.y + bias.y),
+                           activate<ACT>(x.z + bias.z), activate<ACT>(x.w + bias.w));
+    if (p.res_dtype >= 0) {
+      const float4 r = residual_of(b.w[i], p.res_dtype);
+      y.x += r.x; y.y += r.y; y.z += r.z; y.w += r.w;
+    }
+    store4_as(p.out, p.out_dtype, i0 + i * is, y);
+  }
+}
+// The same where rows allow no vectors (odd strides) or columns run out (N no multiple of 4): one
+// column n of V rows.
+template <int ACT, int V, typename Sums>
+__device__ __forceinline__ void finish_column(const LinearKernelArgs& p, int64_t m, int n, int r0,
+                                              int step, int cnt, Sums sums) {
+  if (n >= p.N) return;
+  const float bias = p.bias ? p.bias[n] : 0.f;
+  for (int r = r0; r < cnt; r += V * step) {
+    const int64_t ri = (m + r) * p.ldr + n, oi = (m + r) * p.ldo + n;
+    uint32_t w[V];
+    if (p.res_dtype == GDN_F32) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (r + i * step < cnt)
+          w[i] = static_cast<const uint32_t*>(p.residual)[ri + i * step * p.ldr];
+    } else if (p.res_dtype >= 0) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (r + i * step < cnt)
+          w[i] = static_cast<const uint16_t*>(p.residual)[ri + i * step * p.ldr];
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (r + i * step >= cnt) break;
+      float y = activate<ACT>(sums(r + i * step) + bias);
+      if (p.res_dtype >= 0) {
+        const uint32_t u[4] = {w[i], 0u, 0u, 0u};
+        y += residual_of(u, p.res_dtype).x;
+      }
+      store1_as(p.out, p.out_dtype, oi + i * step * p.ldo, y);
     }
   }
 }
-template <int ACT, typename TR, typename Sums>
-__device__ __forceinline__ void finish_o(const LinearKernelArgs& p, int64_t m, int n, int r0,
-                                         int step, int cnt, Sums sums) {
-  if (p.out_dtype == GDN_BF16) finish_rows<ACT, TR, __nv_bfloat16>(p, m, n, r0, step, cnt, sums);
-  else if (p.out_dtype == GDN_F32) finish_rows<ACT, TR, float>(p, m, n, r0, step, cnt, sums);
-  else finish_rows<ACT, TR, __half>(p, m, n, r0, step, cnt, sums);
-}
-template <int ACT, typename Sums>
-__device__ __forceinline__ void finish_r(const LinearKernelArgs& p, int64_t m, int n, int r0,
-                                         int step, int cnt, Sums sums) {
-  if (p.res_dtype < 0) finish_o<ACT, NoResidual>(p, m, n, r0, step, cnt, sums);
-  else if (p.res_dtype == GDN_BF16) finish_o<ACT, __nv_bfloat16>(p, m, n, r0, step, cnt, sums);
-  else if (p.res_dtype == GDN_F32) finish_o<ACT, float>(p, m, n, r0, step, cnt, sums);
-  else finish_o<ACT, __half>(p, m, n, r0, step, cnt, sums);
-}
-template <typename Sums>
-__device__ __forceinline__ void finish(const LinearKernelArgs& p, int64_t m, int n, int r0, int step,
-                                       int cnt, Sums sums) {
-  if (p.act == GDN_ACT_NONE) finish_r<GDN_ACT_NONE>(p, m, n, r0, step, cnt, sums);
-  else if (p.act == GDN_ACT_SILU) finish_r<GDN_ACT_SILU>(p, m, n, r0, step, cnt, sums);
-  else if (p.act == GDN_ACT_GELU) finish_r<GDN_ACT_GELU>(p, m, n, r0, step, cnt, sums);
-  else finish_r<GDN_ACT_SIGMOID>(p, m, n, r0, step, cnt, sums);
+__device__ __forceinline__ float4 bias_at(const LinearKernelArgs& p, int n) {
+  float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (p.bias && n + 4 <= p.N) { b.x = p.bias[n]; b.y = p.bias[n + 1]; b.z = p.bias[n + 2]; b.w = p.bias[n + 3]; }
+  return b;
 }
 
 // ---------------------------------------------------------------- clusters
@@ -184,9 +210,9 @@ constexpr int lt_stages(int bm) { return bm <= 16 ? 5 : bm <= 32 ? 5 : bm <= 64 
 constexpr int lt_sums(int bm) { return bm * LN_BN * 4; }  // the partial sums of the whole tile
 constexpr int lt_smem(int bm) { return lt_stages(bm) * lt_stage(bm) + lt_sums(bm) + 1024; }
 
-template <int BM>
+template <int BM, int ACT>
 __global__ void __launch_bounds__(LN_THREADS, 1)
-linear_tile_kernel(const LinearKernelArgs p, const __grid_constant__ CUtensorMap tm_w,
+linear_tile_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_constant__ CUtensorMap tm_w,
                    const __grid_constant__ CUtensorMap tm_x) {
   constexpr int NST = lt_stages(BM), SB = lt_stage(BM), SUB = lt_sub(BM), BK = 64 * SUB;
   constexpr uint32_t TCOLS = BM < 32 ? 32 : BM;
@@ -267,14 +293,27 @@ linear_tile_kernel(const LinearKernelArgs p, const __grid_constant__ CUtensorMap
     }
     __syncwarp();
   }
+  // each warp every fourth token of this rank's share of the tile (rank r: tokens [r per, +per)),
+  // 4 columns per lane; the first residuals and the bias arrive under the main loop
+  const int per = BM / split, per_log = 31 - __clz(per);
+  const int g = lane * 4;
+  const int64_t mr = m0 + (int64_t)rank * per;
+  const int cnt = p.M - mr < per ? (int)(p.M - mr) : per;
+  const bool vec = p.vec && n0 + LN_BN <= p.N;
+  ResBatch res;
+  float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (warp < 4 && vec) {
+    bias = bias_at(p, n0 + g);
+    fetch_rows(p, res, mr, n0 + g, warp, 4, cnt);
+  }
+
   // the accumulator is complete
   if (!mbar_wait(&done, 0, nullptr)) failed = 1;
   fence_after_sync();
   if (split > 1) cluster_wait();  // the other CTAs' barriers are ready
 
-  // every token's partial sums to the rank that finishes it: rank r the tokens [r per, (r + 1) per)
-  const int per = BM / split, per_log = 31 - __clz(per);
   if (warp < 4) {
+    // every token's partial sums to the rank that finishes it
     const int tokens = (int)(p.M - m0 < BM ? p.M - m0 : BM);
     const uint32_t mine = smem_u32(sums + rank * per * LN_BN + warp * 32 + lane);
     for (int c = 0; c < BM && c < tokens; c += 16) {
@@ -299,24 +338,236 @@ linear_tile_kernel(const LinearKernelArgs p, const __grid_constant__ CUtensorMap
       if (lane < split) arrive_cluster(at_rank(smem_u32(&joined), lane));
       if (!wait_cluster(&joined, 0)) failed = 1;
     }
-    // each warp every fourth token of this rank's share, 4 columns per lane
-    const int g = lane * 4;
-    const int64_t mr = m0 + (int64_t)rank * per;
-    const int cnt = p.M - mr < per ? (int)(p.M - mr) : per;
-    if (!failed)
-      finish(p, mr, n0 + g, warp, 4, cnt, [&](int t) {
-        float4 v = *reinterpret_cast<const float4*>(sums + t * LN_BN + g);
-        for (int s = 1; s < split; ++s) {
-          const float4 x = *reinterpret_cast<const float4*>(sums + (s * per + t) * LN_BN + g);
-          v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
-        }
-        return v;
-      });
+    if (!failed && vec) {
+#pragma unroll 1
+      for (int r = warp; r < cnt; r += 4 * EP_ROWS) {
+        if (r != warp) fetch_rows(p, res, mr, n0 + g, r, 4, cnt);
+        finish_rows<ACT>(p, res, mr, n0 + g, r, 4, cnt, bias, [&](int t) {
+          float4 v = *reinterpret_cast<const float4*>(sums + t * LN_BN + g);
+          for (int s = 1; s < split; ++s) {
+            const float4 x = *reinterpret_cast<const float4*>(sums + (s * per + t) * LN_BN + g);
+            v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+          }
+          return v;
+        });
+      }
+    } else if (!failed) {
+#pragma unroll 1
+      for (int c = lane; c < LN_BN; c += 32)
+        finish_column<ACT, 8>(p, mr, n0 + c, warp, 4, cnt, [&](int t) {
+          float v = sums[t * LN_BN + c];
+          for (int s = 1; s < split; ++s) v += sums[(s * per + t) * LN_BN + c];
+          return v;
+        });
+    }
   }
   fence_before_sync();
   __syncthreads();
   if (failed && tid == 0) set_status(p.status, GDN_ETIMEOUT);
   if (warp == 5) tmem_dealloc(tm, TCOLS);
+}
+
+// ---------------------------------------------------------------- pair kernel
+// Two CTAs on neighbouring SMs work on one 256 x 256 output tile (cta_group::2): CTA r of the pair
+// loads tokens [128 r, +128) of x and columns [128 r, +128) of w and holds the accumulator rows of
+// its tokens; the leader (rank 0) issues every MMA for both. Per 64 K elements a CTA fetches 32 KB
+// for 512 cycles of MMA, 64 bytes per cycle, where a one-CTA 128 x 256 tile would fetch 96 and run
+// into what L2 delivers (about 80 to 90 per SM, measured). Persistent: the pairs walk the tiles, the
+// two halves of tensor memory alternate as accumulators, and the epilogue of one tile runs under
+// the MMAs of the next.
+constexpr int LP_T = 256;       // tokens and output columns of a tile
+constexpr int LP_STAGES = 6;
+constexpr int LP_HALF = 128 * 128;          // bytes of one operand's half tile of a stage
+constexpr int LP_STAGE = 2 * LP_HALF;       // this CTA's x and w rows
+constexpr int LP_OUT = 4 * 32 * 128;        // per epilogue warp 32 rows x 32 fp32
+constexpr int LP_SMEM = LP_STAGES * LP_STAGE + LP_OUT + 1024;
+constexpr int LP_GROUP = 8;     // token tiles walked together, so that pairs share tiles in L2
+
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int x, int y,
+                                              uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];"
+      :
+      : "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
+      :
+      : "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+// Arrive on `bar` of both CTAs of the pair when the MMAs issued so far have completed.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;"
+      :
+      : "r"(smem_u32(bar)), "h"((uint16_t)3)
+      : "memory");
+}
+
+// Token tile and column tile of the t-th tile: groups of LP_GROUP token tiles, column by column.
+__device__ __forceinline__ void tile_at(int64_t t, int64_t mt, int nt, int64_t* im, int* in) {
+  const int64_t per = (int64_t)LP_GROUP * nt, g = t / per, first = g * LP_GROUP;
+  const int64_t rows = mt - first < LP_GROUP ? mt - first : LP_GROUP;
+  const int64_t r = t - g * per;
+  *im = first + r % rows;
+  *in = (int)(r / rows);
+}
+
+template <int ACT>
+__global__ void __launch_bounds__(LN_THREADS, 1)
+linear_pair_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_constant__ CUtensorMap tm_w,
+                   const __grid_constant__ CUtensorMap tm_x) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~static_cast<uintptr_t>(1023));
+  __shared__ uint64_t full[LP_STAGES], empty[LP_STAGES], tfull[2], tempty[2];
+  __shared__ uint32_t tmem_base;
+  __shared__ int failed;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int rank = blockIdx.x & 1;
+  const int64_t mt = (p.M + LP_T - 1) / LP_T;
+  const int nt = (p.N + LP_T - 1) / LP_T;
+  const int64_t tiles = mt * nt;
+  const int64_t pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+  const int ksteps = (p.K + 63) / 64;
+
+  if (tid == 0) {
+    for (int i = 0; i < LP_STAGES; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&tfull[i], 1); mbar_init(&tempty[i], 8); }
+    failed = 0;
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_u32(&tmem_base))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  fence_before_sync();
+  __syncthreads();
+  cluster_arrive();
+  cluster_wait();  // both CTAs' barriers and tensor memory are ready
+  fence_after_sync();
+  const uint32_t tm = tmem_base;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  if (warp == 4) {
+    if (elect_one()) {
+      int st = 0, i = 0;
+      uint32_t ph = 1;  // the ring starts empty
+      for (int64_t t = pair; t < tiles && !failed; t += pairs) {
+        int64_t im; int in;
+        tile_at(t, mt, nt, &im, &in);
+        const int xr = (int)(im * LP_T) + rank * 128, wr = in * LP_T + rank * 128;
+        for (int k = 0; k < ksteps; ++k, ++i) {
+          if (!mbar_wait(&empty[st], ph, &failed)) { failed = 1; break; }
+          // both CTAs' copies count on the leader's barrier
+          if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * LP_STAGE);
+          const uint32_t bar = at_rank(smem_u32(&full[st]), 0);
+          tma_load_pair(sm + st * LP_STAGE, &tm_x, k * 64, xr, bar);
+          tma_load_pair(sm + st * LP_STAGE + LP_HALF, &tm_w, k * 64, wr, bar);
+          if (++st == LP_STAGES) { st = 0; ph ^= 1; }
+        }
+      }
+      // after a time-out: the copies of the pair may still be in flight; the leader waits for
+      // those that it still counts, the other CTA stays until the leader is through (below)
+      if (failed && rank == 0)
+        for (int j = i > LP_STAGES ? i - LP_STAGES : 0; j < i; ++j)
+          mbar_wait(&full[j % LP_STAGES], (j / LP_STAGES) & 1, nullptr);
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    if (rank == 0 && elect_one()) {
+      int st = 0, buf = 0;
+      uint32_t ph = 0, tph = 1;
+      for (int64_t t = pair; t < tiles && !failed; t += pairs) {
+        if (!mbar_wait(&tempty[buf], tph, &failed)) { failed = 1; break; }
+        fence_after_sync();
+        const uint32_t d = tm + buf * LP_T;
+        for (int k = 0; k < ksteps; ++k) {
+          if (!mbar_wait(&full[st], ph, &failed)) { failed = 1; break; }
+          fence_after_sync();
+          const uint32_t a = smem_u32(sm + st * LP_STAGE);
+          const uint64_t da = desc_sw128(a, 16, 1024), db = desc_sw128(a + LP_HALF, 16, 1024);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mma_pair(d, da + 2 * q, db + 2 * q, p.idesc, k > 0 || q > 0);
+          commit_pair(&empty[st]);
+          if (++st == LP_STAGES) { st = 0; ph ^= 1; }
+        }
+        commit_pair(&tfull[buf]);
+        if (++buf == 2) { buf = 0; tph ^= 1; }
+      }
+    }
+    __syncwarp();
+  } else {
+    float* stage = reinterpret_cast<float*>(sm + LP_STAGES * LP_STAGE) + warp * 32 * 32;
+    const int q4 = lane & 7;
+    int buf = 0;
+    uint32_t ph = 0;
+#pragma unroll 1
+    for (int64_t t = pair; t < tiles; t += pairs) {
+      int64_t im; int in;
+      tile_at(t, mt, nt, &im, &in);
+      const int64_t m = im * LP_T + rank * 128 + warp * 32;
+      const int n0 = in * LP_T;
+      const int cnt = m >= p.M ? 0 : p.M - m < 32 ? (int)(p.M - m) : 32;
+      if (!mbar_wait(&tfull[buf], ph, &failed)) { failed = 1; break; }
+      fence_after_sync();
+#pragma unroll 1
+      for (int c = 0; c < LP_T && n0 + c < p.N && cnt > 0; c += 32) {
+        const int n = n0 + c + q4 * 4;
+        const bool vec = p.vec && n0 + c + 32 <= p.N;
+        ResBatch res;
+        float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (vec) {
+          bias = bias_at(p, n);
+          fetch_rows(p, res, m, n, lane >> 3, 4, cnt);
+        }
+        uint32_t r[32];
+        tmem_ld32(taddr(tm, warp * 32, buf * LP_T + c), r);
+        tmem_wait_ld();
+        __syncwarp();  // the previous 32 columns have been read
+        // row = lane; 16-byte groups swizzled by the row, so that rows written by a quarter-warp
+        // and groups read by one both cover all banks
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<float4*>(stage + lane * 32 + ((j ^ (lane & 7)) << 2)) =
+              make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                          __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
+        __syncwarp();
+        if (vec)
+          finish_rows<ACT>(p, res, m, n, lane >> 3, 4, cnt, bias, [&](int row) {
+            return *reinterpret_cast<const float4*>(stage + row * 32 + ((q4 ^ (row & 7)) << 2));
+          });
+        else
+          finish_column<ACT, 16>(p, m, n0 + c + lane, 0, 1, cnt, [&](int row) {
+            return stage[row * 32 + (((lane >> 2) ^ (row & 7)) << 2) + (lane & 3)];
+          });
+      }
+      // this warp has read its part of the accumulator
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(at_rank(smem_u32(&tempty[buf]), 0));
+      if (++buf == 2) { buf = 0; ph ^= 1; }
+    }
+    __syncwarp();
+  }
+  fence_before_sync();
+  __syncthreads();
+  if (failed && tid == 0) set_status(p.status, GDN_ETIMEOUT);
+  cluster_arrive();
+  cluster_wait();  // the leader's MMAs read this CTA's stages, the epilogues signal the leader
+  if (warp == 5)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
 }
 
 // ------------------------------------------------------------------------------- host side
@@ -370,14 +621,14 @@ LinearKernelArgs kernel_args(const LinearArgs& a) {
   return k;
 }
 
-template <int BM>
+template <int BM, int ACT>
 cudaError_t launch_tile(const LinearArgs& a, int sms, cudaStream_t s) {
   const bool bf16 = a.dtype == GDN_BF16;
   alignas(64) CUtensorMap tm_w, tm_x;
   cudaError_t e = make_map(&tm_w, a.w, bf16, a.N, a.K, a.ldw, LN_BN);
   if (e == cudaSuccess) e = make_map(&tm_x, a.x, bf16, a.M, a.K, a.ldx, BM);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(linear_tile_kernel<BM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(linear_tile_kernel<BM, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              lt_smem(BM));
   if (e != cudaSuccess) return e;
   const int64_t nt = (a.N + LN_BN - 1) / LN_BN, mt = (a.M + BM - 1) / BM;
@@ -403,7 +654,48 @@ cudaError_t launch_tile(const LinearArgs& a, int sms, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, linear_tile_kernel<BM>, k, tm_w, tm_x);
+  return cudaLaunchKernelEx(&cfg, linear_tile_kernel<BM, ACT>, k, tm_w, tm_x);
+}
+
+template <int ACT>
+cudaError_t launch_pair(const LinearArgs& a, int sms, cudaStream_t s) {
+  const bool bf16 = a.dtype == GDN_BF16;
+  alignas(64) CUtensorMap tm_w, tm_x;
+  cudaError_t e = make_map(&tm_w, a.w, bf16, a.N, a.K, a.ldw, 128);
+  if (e == cudaSuccess) e = make_map(&tm_x, a.x, bf16, a.M, a.K, a.ldx, 128);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(linear_pair_kernel<ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             LP_SMEM);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = ((a.M + LP_T - 1) / LP_T) * ((a.N + LP_T - 1) / LP_T);
+  const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
+  LinearKernelArgs k = kernel_args(a);
+  k.idesc = idesc_f16(LP_T, LP_T, false, false) | (bf16 ? (1u << 7) | (1u << 10) : 0u);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * pairs));
+  cfg.blockDim = dim3(LN_THREADS);
+  cfg.dynamicSmemBytes = LP_SMEM;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, linear_pair_kernel<ACT>, k, tm_w, tm_x);
+}
+
+template <int ACT>
+cudaError_t launch_act(const LinearArgs& a, int sms, cudaStream_t s) {
+  if (a.M <= 16) return launch_tile<16, ACT>(a, sms, s);
+  if (a.M <= 32) return launch_tile<32, ACT>(a, sms, s);
+  if (a.M <= 64) return launch_tile<64, ACT>(a, sms, s);
+  const int64_t t128 = ((a.M + 127) / 128) * ((a.N + 127) / 128);
+  if (t128 <= sms) return launch_tile<128, ACT>(a, sms, s);
+  return launch_pair<ACT>(a, sms, s);
 }
 
 }  // namespace
@@ -413,10 +705,12 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  if (a.M <= 16) return launch_tile<16>(a, sms, s);
-  if (a.M <= 32) return launch_tile<32>(a, sms, s);
-  if (a.M <= 64) return launch_tile<64>(a, sms, s);
-  return launch_tile<128>(a, sms, s);
+  switch (a.act) {
+    case GDN_ACT_SILU: return launch_act<GDN_ACT_SILU>(a, sms, s);
+    case GDN_ACT_GELU: return launch_act<GDN_ACT_GELU>(a, sms, s);
+    case GDN_ACT_SIGMOID: return launch_act<GDN_ACT_SIGMOID>(a, sms, s);
+  }
+  return launch_act<GDN_ACT_NONE>(a, sms, s);
 }
 
 }  // namespace gdn
