@@ -28,7 +28,8 @@ namespace {
 
 using namespace umma;
 
-constexpr int LN_THREADS = 192;  // warps 0-3 epilogue (TMEM lanes 32 w ..), 4 TMA, 5 MMA
+// Epilogue warps 0 .. EPI - 1 (TMEM lanes 32 (w % 4) ..), then the TMA warp and the MMA warp.
+constexpr int ln_threads(int epi) { return (epi + 2) * 32; }
 constexpr int LN_BN = 128;       // output columns per tile
 
 struct LinearKernelArgs {
@@ -55,28 +56,18 @@ __device__ __forceinline__ float activate(float v) {
   if constexpr (ACT == GDN_ACT_SIGMOID) return sigmoidf_(v);
   return v;
 }
-__device__ __forceinline__ void store4_as(void* base, int dtype, int64_t i, float4 v) {
-  if (dtype == GDN_BF16) st4(static_cast<__nv_bfloat16*>(base) + i, v);
-  else if (dtype == GDN_F32) st4(static_cast<float*>(base) + i, v);
-  else st4(static_cast<__half*>(base) + i, v);
-}
-__device__ __forceinline__ void store1_as(void* base, int dtype, int64_t i, float v) {
-  if (dtype == GDN_BF16) st(static_cast<__nv_bfloat16*>(base) + i, v);
-  else if (dtype == GDN_F32) st(static_cast<float*>(base) + i, v);
-  else st(static_cast<__half*>(base) + i, v);
-}
-
 // Residuals are fetched as raw bits, all loads of a batch before the first use, and ahead of the
 // sums that they are added to.
-constexpr int EP_ROWS = 8;  // rows of a batch of 4-column vectors
-struct ResBatch { uint32_t w[EP_ROWS][4]; };
-__device__ __forceinline__ void fetch_rows(const LinearKernelArgs& p, ResBatch& b, int64_t m, int n,
+template <int V>
+struct ResBatch { uint32_t w[V][4]; };
+template <int V>
+__device__ __forceinline__ void fetch_rows(const LinearKernelArgs& p, ResBatch<V>& b, int64_t m, int n,
                                            int r0, int step, int cnt) {
   if (p.res_dtype < 0 || !p.vec || n + 4 > p.N) return;
   const int64_t i0 = (m + r0) * p.ldr + n, is = p.ldr * step;
   if (p.res_dtype == GDN_F32) {
 #pragma unroll
-    for (int i = 0; i < EP_ROWS; ++i)
+    for (int i = 0; i < V; ++i)
       if (r0 + i * step < cnt) {
         const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const float*>(p.residual) + i0 +
                                                         i * is);
@@ -84,7 +75,7 @@ __device__ __forceinline__ void fetch_rows(const LinearKernelArgs& p, ResBatch& 
       }
   } else {
 #pragma unroll
-    for (int i = 0; i < EP_ROWS; ++i)
+    for (int i = 0; i < V; ++i)
       if (r0 + i * step < cnt) {
         const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.residual) +
                                                         i0 + i * is);
@@ -92,68 +83,105 @@ __device__ __forceinline__ void fetch_rows(const LinearKernelArgs& p, ResBatch& 
       }
   }
 }
-__device__ __forceinline__ float4 residual_of(const uint32_t (&w)[4], int dtype) {
-  if (dtype == GDN_F32)
-    return make_float4(__uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2]),
-                       __uint_as_float(w[3]));
-  if (dtype == GDN_BF16)  // a bf16 is the upper half of the fp32 with the same bits
-    return make_float4(__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xffff0000u),
-                       __uint_as_float(w[1] << 16), __uint_as_float(w[1] & 0xffff0000u));
-  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w[0]));
-  const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&w[1]));
-  return make_float4(a.x, a.y, c.x, c.y);
-}
-// Rows r0, r0 + step, .. (EP_ROWS of them, below cnt) of a tile whose row 0 is output row m, the 4
-// columns n .. n + 3 of each, from sums(row) -> float4.
-template <int ACT, typename Sums>
-__device__ __forceinline__ void finish_rows(const LinearKernelArgs& p, const ResBatch& b, int64_t m,
-                                            int n, int r0, int step, int cnt, float4 bias,
-                                            Sums sums) {
-  const int64_t i0 = (m + r0) * p.ldo + n, is = p.ldo * step;
+// The batch's bits as fp32, one switch for all rows (zeros without a residual).
+template <int V, int W>
+__device__ __forceinline__ void residual_values(uint32_t (&w)[V][W], float (&y)[V][W], int dtype) {
+  if (dtype < 0) {
 #pragma unroll
-  for (int i = 0; i < EP_ROWS; ++i) {
-    if (r0 + i * step >= cnt) break;
-    const float4 x = sums(r0 + i * step);
-    float4 y = make_float4(activate<ACT>(x.x + bias.x), activate<ACT>(x.y + bias.y),
-                           activate<ACT>(x.z + bias.z), activate<ACT>(x.w + bias.w));
-    if (p.res_dtype >= 0) {
-      const float4 r = residual_of(b.w[i], p.res_dtype);
-      y.x += r.x; y.y += r.y; y.z += r.z; y.w += r.w;
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < W; ++j) y[i][j] = 0.f;
+  } else if (dtype == GDN_F32) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < W; ++j) y[i][j] = __uint_as_float(w[i][j]);
+  } else if (dtype == GDN_BF16) {  // a bf16 is the upper half of the fp32 with the same bits
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if constexpr (W == 4) { y[i][3] = __uint_as_float(w[i][1] & 0xffff0000u); y[i][2] = __uint_as_float(w[i][1] << 16); y[i][1] = __uint_as_float(w[i][0] & 0xffff0000u); }
+      y[i][0] = __uint_as_float(w[i][0] << 16);
     }
-    store4_as(p.out, p.out_dtype, i0 + i * is, y);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w[i][0]));
+      y[i][0] = a.x;
+      if constexpr (W == 4) {
+        const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&w[i][1]));
+        y[i][1] = a.y; y[i][2] = c.x; y[i][3] = c.y;
+      }
+    }
   }
 }
+template <int ACT, int V, typename TO, typename Sums>
+__device__ __forceinline__ void store_rows(TO* out, const float (&y)[V][4], int64_t i0,
+                                           int64_t is, int r0, int step, int cnt, float4 bias,
+                                           Sums sums) {
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (r0 + i * step < cnt) {
+      const float4 x = sums(r0 + i * step);
+      st4(out + i0 + i * is, make_float4(activate<ACT>(x.x + bias.x) + y[i][0],
+                                         activate<ACT>(x.y + bias.y) + y[i][1],
+                                         activate<ACT>(x.z + bias.z) + y[i][2],
+                                         activate<ACT>(x.w + bias.w) + y[i][3]));
+    }
+}
+// Rows r0, r0 + step, .. (V of them, below cnt) of a tile whose row 0 is output row m, the 4
+// columns n .. n + 3 of each, from sums(row) -> float4.
+template <int ACT, int V, typename Sums>
+__device__ __forceinline__ void finish_rows(const LinearKernelArgs& p, ResBatch<V>& b, int64_t m, int n,
+                                            int r0, int step, int cnt, float4 bias, Sums sums) {
+  const int64_t i0 = (m + r0) * p.ldo + n, is = p.ldo * step;
+  float y[V][4];
+  residual_values(b.w, y, p.res_dtype);
+  if (p.out_dtype == GDN_BF16)
+    store_rows<ACT, V>(static_cast<__nv_bfloat16*>(p.out), y, i0, is, r0, step, cnt, bias, sums);
+  else if (p.out_dtype == GDN_F32)
+    store_rows<ACT, V>(static_cast<float*>(p.out), y, i0, is, r0, step, cnt, bias, sums);
+  else
+    store_rows<ACT, V>(static_cast<__half*>(p.out), y, i0, is, r0, step, cnt, bias, sums);
+}
+template <int V, typename TO>
+__device__ __forceinline__ void store_column(TO* out, const float (&y)[V][1], int64_t i0, int64_t is,
+                                             int r0, int step, int cnt) {
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (r0 + i * step < cnt) st(out + i0 + i * is, y[i][0]);
+}
 // The same where rows allow no vectors (odd strides) or columns run out (N no multiple of 4): one
-// column n of V rows.
+// column n, V rows at a time.
 template <int ACT, int V, typename Sums>
 __device__ __forceinline__ void finish_column(const LinearKernelArgs& p, int64_t m, int n, int r0,
                                               int step, int cnt, Sums sums) {
   if (n >= p.N) return;
   const float bias = p.bias ? p.bias[n] : 0.f;
+#pragma unroll 1
   for (int r = r0; r < cnt; r += V * step) {
-    const int64_t ri = (m + r) * p.ldr + n, oi = (m + r) * p.ldo + n;
-    uint32_t w[V];
+    const int64_t ri = (m + r) * p.ldr + n, rs = p.ldr * step;
+    uint32_t w[V][1];
+    float y[V][1];
     if (p.res_dtype == GDN_F32) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (r + i * step < cnt)
-          w[i] = static_cast<const uint32_t*>(p.residual)[ri + i * step * p.ldr];
+        w[i][0] = r + i * step < cnt ? static_cast<const uint32_t*>(p.residual)[ri + i * rs] : 0u;
     } else if (p.res_dtype >= 0) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (r + i * step < cnt)
-          w[i] = static_cast<const uint16_t*>(p.residual)[ri + i * step * p.ldr];
+        w[i][0] = r + i * step < cnt ? static_cast<const uint16_t*>(p.residual)[ri + i * rs] : 0u;
     }
+    residual_values(w, y, p.res_dtype);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      if (r + i * step >= cnt) break;
-      float y = activate<ACT>(sums(r + i * step) + bias);
-      if (p.res_dtype >= 0) {
-        const uint32_t u[4] = {w[i], 0u, 0u, 0u};
-        y += residual_of(u, p.res_dtype).x;
-      }
-      store1_as(p.out, p.out_dtype, oi + i * step * p.ldo, y);
-    }
+    for (int i = 0; i < V; ++i)
+      if (r + i * step < cnt) y[i][0] += activate<ACT>(sums(r + i * step) + bias);
+    const int64_t oi = (m + r) * p.ldo + n, os = p.ldo * step;
+    if (p.out_dtype == GDN_BF16)
+      store_column(static_cast<__nv_bfloat16*>(p.out), y, oi, os, r, step, cnt);
+    else if (p.out_dtype == GDN_F32)
+      store_column(static_cast<float*>(p.out), y, oi, os, r, step, cnt);
+    else
+      store_column(static_cast<__half*>(p.out), y, oi, os, r, step, cnt);
   }
 }
 __device__ __forceinline__ float4 bias_at(const LinearKernelArgs& p, int n) {
@@ -175,8 +203,18 @@ __device__ __forceinline__ uint32_t at_rank(uint32_t local, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
   return remote;
 }
-__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+// Store to another CTA of the cluster (or this one), counted in bytes on that CTA's barrier.
+__device__ __forceinline__ void st_async(uint32_t addr, uint32_t v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];"
+               :
+               : "r"(addr), "r"(v), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void prefetch_2d(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];"
+               :
+               : "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y)
+               : "memory");
 }
 // Arrive on a barrier of another CTA of the cluster, releasing this thread's (and, after
 // __syncwarp, its warp's) earlier writes to it.
@@ -210,12 +248,20 @@ constexpr int lt_stages(int bm) { return bm <= 16 ? 5 : bm <= 32 ? 5 : bm <= 64 
 constexpr int lt_sums(int bm) { return bm * LN_BN * 4; }  // the partial sums of the whole tile
 constexpr int lt_smem(int bm) { return lt_stages(bm) * lt_stage(bm) + lt_sums(bm) + 1024; }
 
+// Up to 16 tokens: 4 epilogue warps and at most 128 registers, so that two CTAs fit on an SM (15 of
+// the GPU's clusters of 8 find place at one CTA per SM, and a 16th would run alone behind them).
+constexpr int lt_epi(int bm) { return bm <= 16 ? 4 : 8; }
+// Rows per batch of the epilogue: few for few tokens, where the length of the code that runs once
+// costs more than its loads in flight gain.
+constexpr int lt_rows(int bm) { return bm <= 16 ? 1 : bm <= 32 ? 2 : bm <= 64 ? 4 : 8; }
+
 template <int BM, int ACT>
-__global__ void __launch_bounds__(LN_THREADS, 1)
+__global__ void __launch_bounds__(BM <= 16 ? 256 : ln_threads(lt_epi(BM)), BM <= 16 ? 2 : 1)
 linear_tile_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_constant__ CUtensorMap tm_w,
                    const __grid_constant__ CUtensorMap tm_x) {
   constexpr int NST = lt_stages(BM), SB = lt_stage(BM), SUB = lt_sub(BM), BK = 64 * SUB;
   constexpr uint32_t TCOLS = BM < 32 ? 32 : BM;
+  constexpr int LN_EPI = lt_epi(BM), LN_TMA = LN_EPI, LN_MMA = LN_EPI + 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
@@ -231,15 +277,20 @@ linear_tile_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
   const int ksteps = (p.K + BK - 1) / BK;
   const int k0 = (int)((int64_t)ksteps * rank / split);
   const int nk = (int)((int64_t)ksteps * (rank + 1) / split) - k0;
+  // rank r finishes the tokens [r per, (r + 1) per) of the tile, of which cnt exist
+  const int per = BM / split, per_log = 31 - __clz(per);
+  const int64_t mr = m0 + (int64_t)rank * per;
+  const int cnt = p.M - mr < per ? (int)(p.M - mr) : per;
 
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
     mbar_init(&done, 1);
-    mbar_init(&joined, 4 * split);
+    mbar_init(&joined, 1);
     failed = 0;
     fence_mbar_init();
+    if (split > 1) mbar_arrive_expect_tx(&joined, (uint32_t)(split * (cnt > 0 ? cnt : 0) * LN_BN * 4));
   }
-  if (warp == 5) {
+  if (warp == LN_MMA) {
     tmem_alloc(&tmem_base, TCOLS);
     tmem_relinquish();  // at once: until then no other block is placed on this SM
   }
@@ -248,10 +299,14 @@ linear_tile_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
   fence_after_sync();
   const uint32_t tm = tmem_base;
   if (split > 1) cluster_arrive();  // the barriers of this CTA are ready (waited for below)
+  // the weights towards L2 while the kernel ahead still runs: no data is read before it has
+  // finished (whatever it may write goes through L2, so nothing stale is kept)
+  if (warp == LN_TMA && elect_one())
+    for (int i = 0; i < nk * SUB && i < NST * SUB; ++i) prefetch_2d(&tm_w, k0 * BK + i * 64, n0);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  if (warp == 4) {
+  if (warp == LN_TMA) {
     if (elect_one()) {
       int i = 0;
       for (; i < nk; ++i) {
@@ -272,7 +327,7 @@ linear_tile_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
           mbar_wait(&full[j % NST], (j / NST) & 1, nullptr);
     }
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == LN_MMA) {
     if (elect_one()) {
       for (int i = 0; i < nk; ++i) {
         const int st = i % NST;
@@ -293,18 +348,16 @@ linear_tile_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
     }
     __syncwarp();
   }
-  // each warp every fourth token of this rank's share of the tile (rank r: tokens [r per, +per)),
-  // 4 columns per lane; the first residuals and the bias arrive under the main loop
-  const int per = BM / split, per_log = 31 - __clz(per);
+  // each warp every eighth token of this rank's share, 4 columns per lane; the first residuals and
+  // the bias arrive under the main loop
   const int g = lane * 4;
-  const int64_t mr = m0 + (int64_t)rank * per;
-  const int cnt = p.M - mr < per ? (int)(p.M - mr) : per;
   const bool vec = p.vec && n0 + LN_BN <= p.N;
-  ResBatch res;
+  constexpr int V = lt_rows(BM);
+  ResBatch<V> res;
   float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (warp < 4 && vec) {
+  if (warp < LN_EPI && vec) {
     bias = bias_at(p, n0 + g);
-    fetch_rows(p, res, mr, n0 + g, warp, 4, cnt);
+    fetch_rows(p, res, mr, n0 + g, warp, LN_EPI, cnt);
   }
 
   // the accumulator is complete
@@ -312,38 +365,38 @@ linear_tile_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
   fence_after_sync();
   if (split > 1) cluster_wait();  // the other CTAs' barriers are ready
 
-  if (warp < 4) {
-    // every token's partial sums to the rank that finishes it
-    const int tokens = (int)(p.M - m0 < BM ? p.M - m0 : BM);
-    const uint32_t mine = smem_u32(sums + rank * per * LN_BN + warp * 32 + lane);
-    for (int c = 0; c < BM && c < tokens; c += 16) {
+  if (warp < LN_EPI) {
+    // every token's partial sums to the rank that finishes it; the two warps of a lane quarter
+    // take alternating groups of 16 tokens
+    const int tokens = (int)(p.M - m0 < BM ? p.M - m0 : BM), col = (warp & 3) * 32 + lane;
+    const uint32_t mine = smem_u32(sums + rank * per * LN_BN + col), jbar = smem_u32(&joined);
+    for (int c = (warp >> 2) * 16; c < BM && c < tokens; c += LN_EPI * 4) {
       uint32_t r[16];
-      tmem_ld16(taddr(tm, warp * 32, c), r);
+      tmem_ld16(taddr(tm, (warp & 3) * 32, c), r);
       tmem_wait_ld();
       if (split == 1) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          sums[(c + i) * LN_BN + warp * 32 + lane] = __uint_as_float(r[i]);
+        for (int i = 0; i < 16; ++i) sums[(c + i) * LN_BN + col] = __uint_as_float(r[i]);
       } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          st_cluster(at_rank(mine + (uint32_t)(((c + i) & (per - 1)) * LN_BN * 4), (c + i) >> per_log),
-                     __uint_as_float(r[i]));
+          if (c + i < tokens) {
+            const int to = (c + i) >> per_log, at = (c + i) & (per - 1);
+            st_async(at_rank(mine + (uint32_t)(at * LN_BN * 4), to), r[i], at_rank(jbar, to));
+          }
       }
     }
-    if (split == 1) {
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-    } else {
-      __syncwarp();
-      if (lane < split) arrive_cluster(at_rank(smem_u32(&joined), lane));
-      if (!wait_cluster(&joined, 0)) failed = 1;
-    }
+    if (split == 1)
+      asm volatile("bar.sync 1, %0;" ::"n"(LN_EPI * 32) : "memory");
+    else if (!wait_cluster(&joined, 0))
+      failed = 1;
     if (!failed && vec) {
 #pragma unroll 1
-      for (int r = warp; r < cnt; r += 4 * EP_ROWS) {
-        if (r != warp) fetch_rows(p, res, mr, n0 + g, r, 4, cnt);
-        finish_rows<ACT>(p, res, mr, n0 + g, r, 4, cnt, bias, [&](int t) {
+      for (int r = warp; r < cnt; r += LN_EPI * V) {
+        if (r != warp) fetch_rows(p, res, mr, n0 + g, r, LN_EPI, cnt);
+        finish_rows<ACT, V>(p, res, mr, n0 + g, r, LN_EPI, cnt, bias, [&](int t) {
           float4 v = *reinterpret_cast<const float4*>(sums + t * LN_BN + g);
+#pragma unroll 1
           for (int s = 1; s < split; ++s) {
             const float4 x = *reinterpret_cast<const float4*>(sums + (s * per + t) * LN_BN + g);
             v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
@@ -354,7 +407,7 @@ linear_tile_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
     } else if (!failed) {
 #pragma unroll 1
       for (int c = lane; c < LN_BN; c += 32)
-        finish_column<ACT, 8>(p, mr, n0 + c, warp, 4, cnt, [&](int t) {
+        finish_column<ACT, 2 * V>(p, mr, n0 + c, warp, LN_EPI, cnt, [&](int t) {
           float v = sums[t * LN_BN + c];
           for (int s = 1; s < split; ++s) v += sums[(s * per + t) * LN_BN + c];
           return v;
@@ -364,7 +417,7 @@ linear_tile_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
   fence_before_sync();
   __syncthreads();
   if (failed && tid == 0) set_status(p.status, GDN_ETIMEOUT);
-  if (warp == 5) tmem_dealloc(tm, TCOLS);
+  if (warp == LN_MMA) tmem_dealloc(tm, TCOLS);
 }
 
 // ---------------------------------------------------------------- pair kernel
@@ -375,11 +428,12 @@ linear_tile_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
 // into what L2 delivers (about 80 to 90 per SM, measured). Persistent: the pairs walk the tiles, the
 // two halves of tensor memory alternate as accumulators, and the epilogue of one tile runs under
 // the MMAs of the next.
+constexpr int LP_EPI = 8;
 constexpr int LP_T = 256;       // tokens and output columns of a tile
 constexpr int LP_STAGES = 6;
 constexpr int LP_HALF = 128 * 128;          // bytes of one operand's half tile of a stage
 constexpr int LP_STAGE = 2 * LP_HALF;       // this CTA's x and w rows
-constexpr int LP_OUT = 4 * 32 * 128;        // per epilogue warp 32 rows x 32 fp32
+constexpr int LP_OUT = LP_EPI * 32 * 128;   // per epilogue warp 32 rows x 32 fp32
 constexpr int LP_SMEM = LP_STAGES * LP_STAGE + LP_OUT + 1024;
 constexpr int LP_GROUP = 8;     // token tiles walked together, so that pairs share tiles in L2
 
@@ -421,9 +475,10 @@ __device__ __forceinline__ void tile_at(int64_t t, int64_t mt, int nt, int64_t* 
 }
 
 template <int ACT>
-__global__ void __launch_bounds__(LN_THREADS, 1)
+__global__ void __launch_bounds__(ln_threads(LP_EPI), 1)
 linear_pair_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_constant__ CUtensorMap tm_w,
                    const __grid_constant__ CUtensorMap tm_x) {
+  constexpr int LN_EPI = LP_EPI, LN_TMA = LN_EPI, LN_MMA = LN_EPI + 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
@@ -441,11 +496,11 @@ linear_pair_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
 
   if (tid == 0) {
     for (int i = 0; i < LP_STAGES; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
-    for (int i = 0; i < 2; ++i) { mbar_init(&tfull[i], 1); mbar_init(&tempty[i], 8); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&tfull[i], 1); mbar_init(&tempty[i], 2 * LN_EPI); }
     failed = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == LN_MMA) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      smem_u32(&tmem_base))
                  : "memory");
@@ -460,7 +515,7 @@ linear_pair_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  if (warp == 4) {
+  if (warp == LN_TMA) {
     if (elect_one()) {
       int st = 0, i = 0;
       uint32_t ph = 1;  // the ring starts empty
@@ -485,7 +540,7 @@ linear_pair_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
           mbar_wait(&full[j % LP_STAGES], (j / LP_STAGES) & 1, nullptr);
     }
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == LN_MMA) {
     if (rank == 0 && elect_one()) {
       int st = 0, buf = 0;
       uint32_t ph = 0, tph = 1;
@@ -510,6 +565,7 @@ linear_pair_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
     __syncwarp();
   } else {
     float* stage = reinterpret_cast<float*>(sm + LP_STAGES * LP_STAGE) + warp * 32 * 32;
+    const int quarter = (warp & 3) * 32, c0 = (warp >> 2) * 128;  // TMEM lanes, columns of the warp
     const int q4 = lane & 7;
     int buf = 0;
     uint32_t ph = 0;
@@ -517,23 +573,23 @@ linear_pair_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
     for (int64_t t = pair; t < tiles; t += pairs) {
       int64_t im; int in;
       tile_at(t, mt, nt, &im, &in);
-      const int64_t m = im * LP_T + rank * 128 + warp * 32;
+      const int64_t m = im * LP_T + rank * 128 + quarter;
       const int n0 = in * LP_T;
       const int cnt = m >= p.M ? 0 : p.M - m < 32 ? (int)(p.M - m) : 32;
       if (!mbar_wait(&tfull[buf], ph, &failed)) { failed = 1; break; }
       fence_after_sync();
 #pragma unroll 1
-      for (int c = 0; c < LP_T && n0 + c < p.N && cnt > 0; c += 32) {
+      for (int c = c0; c < c0 + 128 && n0 + c < p.N && cnt > 0; c += 32) {
         const int n = n0 + c + q4 * 4;
         const bool vec = p.vec && n0 + c + 32 <= p.N;
-        ResBatch res;
+        ResBatch<8> res;
         float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
         if (vec) {
           bias = bias_at(p, n);
           fetch_rows(p, res, m, n, lane >> 3, 4, cnt);
         }
         uint32_t r[32];
-        tmem_ld32(taddr(tm, warp * 32, buf * LP_T + c), r);
+        tmem_ld32(taddr(tm, quarter, buf * LP_T + c), r);
         tmem_wait_ld();
         __syncwarp();  // the previous 32 columns have been read
         // row = lane; 16-byte groups swizzled by the row, so that rows written by a quarter-warp
@@ -545,7 +601,7 @@ linear_pair_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
                           __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
         __syncwarp();
         if (vec)
-          finish_rows<ACT>(p, res, m, n, lane >> 3, 4, cnt, bias, [&](int row) {
+          finish_rows<ACT, 8>(p, res, m, n, lane >> 3, 4, cnt, bias, [&](int row) {
             return *reinterpret_cast<const float4*>(stage + row * 32 + ((q4 ^ (row & 7)) << 2));
           });
         else
@@ -566,7 +622,7 @@ linear_pair_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
   if (failed && tid == 0) set_status(p.status, GDN_ETIMEOUT);
   cluster_arrive();
   cluster_wait();  // the leader's MMAs read this CTA's stages, the epilogues signal the leader
-  if (warp == 5)
+  if (warp == LN_MMA)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
 }
 
@@ -649,7 +705,7 @@ cudaError_t launch_tile(const LinearArgs& a, int sms, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(nt * split), (unsigned)mt);
-  cfg.blockDim = dim3(LN_THREADS);
+  cfg.blockDim = dim3(ln_threads(lt_epi(BM)));
   cfg.dynamicSmemBytes = lt_smem(BM);
   cfg.stream = s;
   cfg.attrs = attr;
@@ -680,7 +736,7 @@ cudaError_t launch_pair(const LinearArgs& a, int sms, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * pairs));
-  cfg.blockDim = dim3(LN_THREADS);
+  cfg.blockDim = dim3(ln_threads(LP_EPI));
   cfg.dynamicSmemBytes = LP_SMEM;
   cfg.stream = s;
   cfg.attrs = attr;
