@@ -78,6 +78,8 @@ _lib = None
 def load(path: str | None = None):
     """Load libgdn.so and declare argument types. Raises if it is not built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -350,7 +350,10 @@ __global__ void __launch_bounds__(DR_THREADS) draft_state_kernel(const DraftArgs
   // ---- the state, before the first kernel's decision on this sequence is known (everything
   // read here was written before that kernel started)
   const int slot = p.slot_ids[n];
-  if (slot < 0 || slot >= p.n_slots) return;
+  if (slot < 0 || slot >= p.n_slots) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // this grid ends after the first one
+    return;
+  }
   const bool rst = p.reset != nullptr && p.reset[n] != 0;
   float* S = p.state + (((int64_t)slot * p.H_v + h) * DK + rg * RPT) * d_v + tile * DR_TILE + cq * 4;
   float4 s[RPT];
@@ -555,8 +558,8 @@ cudaError_t launch_prep(const DraftArgs& a, cudaStream_t s) {
   auto kern = draft_prep_kernel<DK, TX, TS, FUSED>;
   const int bytes = prep_smem(DK, a.H_v / a.H_k);
   if (bytes > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    static std::atomic<int> smem_set[64];
+    const cudaError_t e = allow_smem(kern, bytes, smem_set);
     if (e != cudaSuccess) return e;
   }
   kern<<<dim3(a.H_k, a.n_seqs), DR_THREADS, bytes, s>>>(a);
@@ -586,8 +589,8 @@ cudaError_t launch_state(const DraftArgs& a0, cudaStream_t s) {
   DraftArgs a = a0;
   const int bytes = state_smem(DK, a.rec.depth);
   if (bytes > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    static std::atomic<int> smem_set[64];
+    const cudaError_t e = allow_smem(kern, bytes, smem_set);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchAttribute attr[1];

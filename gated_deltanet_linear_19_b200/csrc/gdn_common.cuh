@@ -123,6 +123,32 @@ int resident_blocks(Kern kern, int threads) {
   return r;
 }
 
+// Raises the dynamic shared memory limit of `kern` on the current device once (the attribute stays
+// with the function; setting it costs about half a microsecond of each call otherwise).
+template <typename Kern>
+cudaError_t allow_smem(Kern kern, int bytes, std::atomic<int>* cache) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool cached = dev >= 0 && dev < 64;
+  if (cached && cache[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && cached) cache[dev].store(bytes, std::memory_order_relaxed);
+  return e;
+}
+// SMs of the current device (0 if unknown), asked for once per device.
+inline int sm_count() {
+  static std::atomic<int> cache[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = cache[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    cache[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 // Packed fp32 pairs (sm_100 f32x2 arithmetic): each lane is one IEEE fp32 operation rounded to
 // nearest, so a lane gives exactly the scalar fmaf / multiply; one instruction does two.
 __device__ __forceinline__ uint64_t pack_f2(float2 v) {

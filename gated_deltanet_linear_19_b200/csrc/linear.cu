@@ -680,12 +680,12 @@ LinearKernelArgs kernel_args(const LinearArgs& a) {
 template <int BM, int ACT>
 cudaError_t launch_tile(const LinearArgs& a, int sms, cudaStream_t s) {
   const bool bf16 = a.dtype == GDN_BF16;
+  static std::atomic<int> smem_set[64];
   alignas(64) CUtensorMap tm_w, tm_x;
   cudaError_t e = make_map(&tm_w, a.w, bf16, a.N, a.K, a.ldw, LN_BN);
   if (e == cudaSuccess) e = make_map(&tm_x, a.x, bf16, a.M, a.K, a.ldx, BM);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(linear_tile_kernel<BM, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             lt_smem(BM));
+    e = allow_smem(linear_tile_kernel<BM, ACT>, lt_smem(BM), smem_set);
   if (e != cudaSuccess) return e;
   const int64_t nt = (a.N + LN_BN - 1) / LN_BN, mt = (a.M + BM - 1) / BM;
   if (mt > 65535) return cudaErrorInvalidValue;
@@ -716,12 +716,12 @@ cudaError_t launch_tile(const LinearArgs& a, int sms, cudaStream_t s) {
 template <int ACT>
 cudaError_t launch_pair(const LinearArgs& a, int sms, cudaStream_t s) {
   const bool bf16 = a.dtype == GDN_BF16;
+  static std::atomic<int> smem_set[64];
   alignas(64) CUtensorMap tm_w, tm_x;
   cudaError_t e = make_map(&tm_w, a.w, bf16, a.N, a.K, a.ldw, 128);
   if (e == cudaSuccess) e = make_map(&tm_x, a.x, bf16, a.M, a.K, a.ldx, 128);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(linear_pair_kernel<ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             LP_SMEM);
+    e = allow_smem(linear_pair_kernel<ACT>, LP_SMEM, smem_set);
   if (e != cudaSuccess) return e;
   const int64_t tiles = ((a.M + LP_T - 1) / LP_T) * ((a.N + LP_T - 1) / LP_T);
   const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
@@ -757,10 +757,8 @@ cudaError_t launch_act(const LinearArgs& a, int sms, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
+  const int sms = sm_count();
+  if (sms == 0) return cudaErrorInvalidDevice;
   switch (a.act) {
     case GDN_ACT_SILU: return launch_act<GDN_ACT_SILU>(a, sms, s);
     case GDN_ACT_GELU: return launch_act<GDN_ACT_GELU>(a, sms, s);
