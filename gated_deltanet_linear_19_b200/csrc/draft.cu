@@ -23,35 +23,78 @@
 //    gates, the tokens' dot products and the two T x T coefficient tables, the accepted keys of
 //    the old record and then the new record's keys, decays and inputs. What the second kernel
 //    needs goes to the workspace (a few KB per head, read from L2).
-//  - draft_state_kernel, one block per (32-column tile, value head, sequence), HBM-bound: the
-//    state tile in registers (loaded before the first kernel has finished), commit, column sums,
-//    the T-step triangular solve per column, o and the record's u.
+//  - draft_state_kernel, HBM-bound, over tiles of up to 64 columns of one (value head, sequence):
+//    commit, column sums, the T-step triangular solve per column, o and the record's u. As many
+//    blocks as fit stay resident and take tiles in turn. A tile's inputs come by asynchronous
+//    copies (TMA for the state, bulk copies for the rest) that are started when the block has
+//    moved the tile before into registers, so that HBM works while the block computes; the first
+//    tile's state is asked for before the first kernel has finished.
 // The keys of a record are shared by the column tiles and value heads of a key head, so they are
 // rewritten by the first kernel, which alone reads them; u belongs to one tile; the count n is
 // read by the first kernel and written by the second. Nothing is read and written by different
 // blocks of one kernel.
+#include <cuda.h>
+
+#include <type_traits>
+
 #include "gdn_common.cuh"
 #include "gdn_internal.h"
+#include "umma.cuh"
 
 namespace gdn {
 namespace {
 
 constexpr int DR_THREADS = 128;
-constexpr int DR_TILE = 32;
 constexpr int DR_MAX = 16;  // tokens per draft, at most
-// per (sequence, value head) in the workspace: Lt[j][i] = beta_i D_ij (k_i.k_j) (j < i),
-// P[i][j] = D_ij (q_i.k_j) (j <= i), then c, beta and the commit weights
-constexpr int DR_COEF = 2 * DR_MAX * DR_MAX + 4 * DR_MAX;
-constexpr int DR_L = 0, DR_P = DR_MAX * DR_MAX, DR_C = 2 * DR_MAX * DR_MAX, DR_BETA = DR_C + DR_MAX,
-              DR_W = DR_BETA + DR_MAX, DR_W0 = DR_W + DR_MAX;
+// Per (sequence, value head) in the workspace, for T tokens padded to TT = token_pad(T):
+// Lt[TT][TT] with Lt[j][i] = beta_i D_ij (k_i.k_j) (j < i), P[TT][TT] with P[i][j] = D_ij (q_i.k_j)
+// (j <= i), zeros elsewhere; c[TT], beta[TT]; the commit weights of the accepted tokens [DR_MAX]
+// and that of the old state.
+__host__ __device__ __forceinline__ int token_pad(int T) { return T <= 4 ? 4 : T <= 8 ? 8 : 16; }
+__host__ __device__ __forceinline__ int coef_size(int T) {
+  const int tt = token_pad(T);
+  return 2 * tt * tt + 2 * tt + DR_MAX + 4;
+}
+constexpr int DR_COEF = 2 * DR_MAX * DR_MAX + 3 * DR_MAX + 4;  // coef_size(DR_MAX)
+
+// A set of the state kernel's second inputs in shared memory (es: bytes of a v element), in floats.
+__host__ __device__ __forceinline__ int late_floats(int d_k, int ct, int depth, int es) {
+  return 2 * depth * d_k + coef_size(depth) + depth * ct * es / 4;
+}
 
 // What the first kernel decides about a sequence.
-struct DraftHeader {
+struct alignas(16) DraftHeader {
   int run;   // 0: skipped (invalid); 1: processed
   int acc;   // accepted tokens of the old record
   int len;   // new tokens
   int rst;   // starts from a zero state
+  int slot;
+  int c0;    // first new token
+  int pad0, pad1;
 };
+
+// x += k s over a quad of columns.
+__device__ __forceinline__ void fma_row(float* x, const float4& s, float k) {
+  x[0] = fmaf(s.x, k, x[0]);
+  x[1] = fmaf(s.y, k, x[1]);
+  x[2] = fmaf(s.z, k, x[2]);
+  x[3] = fmaf(s.w, k, x[3]);
+}
+
+// N consecutive floats (N a multiple of 2, rows of a key's share) from shared memory.
+template <int N>
+__device__ __forceinline__ void load_rows(float* x, const float* from) {
+  if constexpr (N == 2) {
+    const float2 a = *reinterpret_cast<const float2*>(from);
+    x[0] = a.x; x[1] = a.y;
+  } else {
+#pragma unroll
+    for (int m = 0; m < N; m += 4) {
+      const float4 a = *reinterpret_cast<const float4*>(from + m);
+      x[m] = a.x; x[m + 1] = a.y; x[m + 2] = a.z; x[m + 3] = a.w;
+    }
+  }
+}
 
 struct DraftWs {
   size_t hdr, qk, rk, coef, v, o32, total;
@@ -114,7 +157,7 @@ __device__ __forceinline__ void token_dots(const float* vec, float* part) {
 template <int DK, typename TX, typename TS, bool FUSED>
 __global__ void __launch_bounds__(DR_THREADS) draft_prep_kernel(const DraftArgs p) {
   constexpr int LDV = DK + 4, LPH = DK / 4;
-  extern __shared__ __align__(16) float sm[];
+  extern __shared__ __align__(128) float sm[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hk = blockIdx.x, n = blockIdx.y;
   const int r = p.H_v / p.H_k, D = p.rec.depth;
@@ -136,12 +179,12 @@ __global__ void __launch_bounds__(DR_THREADS) draft_prep_kernel(const DraftArgs 
   if (err != 0) {
     if (lead) {
       set_status(p.status, err);
-      *hdr = DraftHeader{0, 0, 0, 0};
+      *hdr = DraftHeader{};
     }
     return;
   }
   const int T = (int)(c1 - c0);
-  if (lead) *hdr = DraftHeader{1, acc, T, rst ? 1 : 0};
+  if (lead) *hdr = DraftHeader{1, acc, T, rst ? 1 : 0, slot, (int)c0, 0, 0};
   const int bs = T <= 4 ? 1 : T <= 8 ? 2 : 4, T4 = 4 * bs;
 
   float* vec = sm;                        // [2 DR_MAX][LDV]: k rows 0..T4-1, q rows T4..2 T4-1
@@ -292,7 +335,7 @@ __global__ void __launch_bounds__(DR_THREADS) draft_prep_kernel(const DraftArgs 
     const float4 kv = *reinterpret_cast<const float4*>(vec + t * LDV + d);
     reinterpret_cast<float4*>(reck)[i] = kv;
     reinterpret_cast<float4*>(qk)[i] = kv;
-    *reinterpret_cast<float4*>(qk + (int64_t)D * DK + i * 4) =
+    *reinterpret_cast<float4*>(qk + (int64_t)T * DK + i * 4) =
         *reinterpret_cast<const float4*>(vec + (T4 + t) * LDV + d);
   }
 
@@ -302,219 +345,359 @@ __global__ void __launch_bounds__(DR_THREADS) draft_prep_kernel(const DraftArgs 
   else token_dots<4, DK>(vec, part);
   __syncthreads();
   float* coef = reinterpret_cast<float*>(ws + p.ws_coef);
-  for (int i = tid; i < r * DR_MAX * DR_MAX; i += DR_THREADS) {
-    const int jv = i / (DR_MAX * DR_MAX), row = (i / DR_MAX) % DR_MAX, col = i % DR_MAX;
+  for (int i = tid; i < r * T4 * T4; i += DR_THREADS) {
+    const int jv = i / (T4 * T4), row = (i / T4) % T4, col = i % T4;
     const int h = (p.layout & GDN_GQA_TILED) ? hk + jv * p.H_k : hk * r + jv;
-    float* cf = coef + ((int64_t)n * p.H_v + h) * DR_COEF;
-    if (row < T && col <= row) {
-      float d = 1.f;
+    float* cL = coef + ((int64_t)n * p.H_v + h) * DR_COEF;
+    float* cP = cL + T4 * T4;
+    float* cC = cP + T4 * T4;
+    const bool in = row < T && col <= row;
+    float d = 1.f, kk = 0.f, qq = 0.f;
+    if (in) {
       for (int l = col + 1; l <= row; ++l) d *= ge[jv * DR_MAX + l];
-      float kk = 0.f, qq = 0.f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         kk += part[(w * 2 * DR_MAX + row) * DR_MAX + col];
         qq += part[(w * 2 * DR_MAX + T4 + row) * DR_MAX + col];
       }
-      cf[DR_P + row * DR_MAX + col] = d * qq;
-      if (col < row) cf[DR_L + col * DR_MAX + row] = gb[jv * DR_MAX + row] * d * kk;
     }
-    if (row == 0) {
-      if (col < T) {
-        float c = 1.f;
-        for (int l = 0; l <= col; ++l) c *= ge[jv * DR_MAX + l];
-        cf[DR_C + col] = c;
-        cf[DR_BETA + col] = gb[jv * DR_MAX + col];
-      }
-      if (col < acc) {
-        float w = 1.f;
-        for (int l = col + 1; l < acc; ++l) w *= go[jv * DR_MAX + l];
-        cf[DR_W + col] = w;
-        if (col == 0) cf[DR_W0] = w * go[jv * DR_MAX];
-      }
+    cP[row * T4 + col] = in ? d * qq : 0.f;
+    cL[col * T4 + row] = in && col < row ? gb[jv * DR_MAX + row] * d * kk : 0.f;
+    if (row == 0 && col < T) {
+      float c = 1.f;
+      for (int l = 0; l <= col; ++l) c *= ge[jv * DR_MAX + l];
+      cC[col] = c;
+      cC[T4 + col] = gb[jv * DR_MAX + col];
     }
+  }
+  for (int i = tid; i < r * acc; i += DR_THREADS) {
+    const int jv = i / acc, j = i - jv * acc;
+    const int h = (p.layout & GDN_GQA_TILED) ? hk + jv * p.H_k : hk * r + jv;
+    float* cW = coef + ((int64_t)n * p.H_v + h) * DR_COEF + 2 * T4 * T4 + 2 * T4;
+    float w = 1.f;
+    for (int l = j + 1; l < acc; ++l) w *= go[jv * DR_MAX + l];
+    cW[j] = w;
+    if (j == 0) cW[DR_MAX] = w * go[jv * DR_MAX];
   }
 }
 
-// TV: v; TO: o.
-template <int DK, typename TV, typename TO>
-__global__ void __launch_bounds__(DR_THREADS) draft_state_kernel(const DraftArgs p) {
-  constexpr int RPT = DK / 16;  // state rows per thread: rg RPT .. + RPT - 1
-  extern __shared__ __align__(16) float sm[];
+// One (column tile, value head, sequence) of the state kernel's work.
+struct DraftTile {
+  int n, h, ct;  // sequence, value head, column tile
+  bool loaded;   // its copies are under way
+  DraftHeader hd;
+};
+__device__ __forceinline__ DraftTile tile_at(const DraftArgs& p, unsigned t, int tiles_c) {
+  const unsigned per = (unsigned)(p.H_v * tiles_c);
+  DraftTile w;
+  w.n = (int)(t / per);
+  const unsigned rem = t - (unsigned)w.n * per;
+  w.h = (int)(rem / (unsigned)tiles_c);
+  w.ct = (int)(rem - (unsigned)w.h * (unsigned)tiles_c);
+  return w;
+}
+__device__ __forceinline__ DraftHeader header_at(const DraftArgs& p, int n) {
+  const int4* g = reinterpret_cast<const int4*>(static_cast<const uint8_t*>(p.workspace) + p.ws_hdr) +
+                  2 * (int64_t)n;
+  const int4 a = g[0], b = g[1];
+  return DraftHeader{a.x, a.y, a.z, a.w, b.x, b.y, 0, 0};
+}
+// A sequence without accepted and without new tokens needs no state, unless it starts from zero.
+__device__ __forceinline__ bool tile_works(const DraftHeader& h) {
+  return h.run && (h.acc > 0 || h.len > 0 || h.rst);
+}
+
+template <int DK, int CT, int MAXT>
+__global__ void __launch_bounds__(DR_THREADS, MAXT <= 8 ? 4 : 2)
+    draft_state_kernel(const DraftArgs p, const __grid_constant__ CUtensorMap tm_state) {
+  constexpr int RPT = DK * CT / (4 * DR_THREADS);  // state rows of a thread
+  constexpr int QL = CT / 4, NRW = 32 / QL;        // lanes per row, row groups of a warp
+  constexpr int TEAMS = DR_THREADS / CT;           // threads per column in the solve
+  constexpr int G = MAXT / 2;                      // tokens summed between two barriers
+  extern __shared__ __align__(128) float sm[];
+  __shared__ __align__(8) uint64_t full;
+  __shared__ DraftTile tiles[2];  // this tile and the next
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int cq = tid & 7, rg = tid >> 3;
-  const int tile = blockIdx.x, h = blockIdx.y, n = blockIdx.z;
-  const int hk = khead_of(h, p.H_k, p.H_v, p.layout);
-  const int d_v = p.d_v, D = p.rec.depth;
+  const int cq = tid % QL, row0 = (tid / QL) * RPT;
+  const int D = p.rec.depth, d_v = p.d_v, tiles_c = d_v / CT;
+  const unsigned total = (unsigned)p.n_seqs * (unsigned)(p.H_v * tiles_c);
   const uint8_t* ws = static_cast<const uint8_t*>(p.workspace);
+  const int es = p.qkv_dtype == GDN_F32 ? 4 : 2;
 
-  // ---- the state, before the first kernel's decision on this sequence is known (everything
-  // read here was written before that kernel started)
-  const int slot = p.slot_ids[n];
-  if (slot < 0 || slot >= p.n_slots) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // this grid ends after the first one
-    return;
-  }
-  const bool rst = p.reset != nullptr && p.reset[n] != 0;
-  float* S = p.state + (((int64_t)slot * p.H_v + h) * DK + rg * RPT) * d_v + tile * DR_TILE + cq * 4;
-  float4 s[RPT];
-  // nothing new and nothing accepted: the state is not needed
-  const bool idle = cu_at(p.cu_seqlens, n + 1) == cu_at(p.cu_seqlens, n) &&
-                    (!p.accepted || p.accepted[n] == 0);
-#pragma unroll
-  for (int m = 0; m < RPT; ++m)
-    s[m] = rst || idle ? make_float4(0.f, 0.f, 0.f, 0.f) : ld4_stream(S + (int64_t)m * d_v);
-  prefetch_state_ahead<DK>(p.state, p.slot_ids, p.n_slots, p.H_v, d_v, p.pf_dist);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float* st_s = sm;               // [DK][CT] state
+  float* rk_s = st_s + DK * CT;   // [D][DK] accepted keys
+  float* uo_s = rk_s + D * DK;    // [D][CT] their u
+  // two sets of: keys and queries [2][T][DK], coefficients, v [T][CT] in its own type. Rows up to
+  // the next multiple of 4 tokens are read (what they give is dropped): at most 3 DK floats behind
+  // the last set's queries, all inside this block's memory.
+  float* late = uo_s + D * CT;
+  const int late_sz = late_floats(DK, CT, D, es);
+  float* red = late + 2 * late_sz;  // [4 warps][k, q][G][CT]
 
-  const DraftHeader hd = *(reinterpret_cast<const DraftHeader*>(ws + p.ws_hdr) + n);
-  if (!hd.run) return;
-  const int T = hd.len, acc = hd.acc;
-  if (tid == 0 && h == 0 && tile == 0) p.rec.n[slot] = T;
-
-  float* qk_s = sm;                        // [2][D][DK]
-  float* rk_s = qk_s + 2 * D * DK;         // [D][DK]
-  float* u_s = rk_s + D * DK;              // [D][DR_TILE]
-  float* red = u_s + D * DR_TILE;          // [4 warps][2 D4][DR_TILE], D4 = D rounded up to 4
-  const int D4 = (D + 3) & ~3;
-  float* cf = red + 4 * 2 * D4 * DR_TILE;  // [DR_COEF]
-  float* recu = p.rec.u + ((int64_t)slot * p.H_v + h) * D * d_v + tile * DR_TILE;
-  {
-    const float4* qk = reinterpret_cast<const float4*>(
-        reinterpret_cast<const float*>(ws + p.ws_qk) + ((int64_t)n * p.H_k + hk) * 2 * D * DK);
-    const float4* rk = reinterpret_cast<const float4*>(
-        reinterpret_cast<const float*>(ws + p.ws_rk) + ((int64_t)n * p.H_k + hk) * D * DK);
-    for (int i = tid; i < T * DK / 4; i += DR_THREADS) {
-      reinterpret_cast<float4*>(qk_s)[i] = qk[i];
-      reinterpret_cast<float4*>(qk_s)[D * DK / 4 + i] = qk[D * DK / 4 + i];
+  // Loads of a tile, by warp 0: the state (unless the first tile has asked for it already) and
+  // the rest of what its sequence needs, all counted on `full`.
+  auto load_tile = [&](const DraftTile& w, int set, bool with_state) {
+    const int T = w.hd.len, acc = w.hd.acc;
+    float* qk = late + set * late_sz;
+    float* cf = qk + 2 * D * DK;
+    uint8_t* vs = reinterpret_cast<uint8_t*>(cf + coef_size(D));
+    const int cbytes = coef_size(T) * 4;
+    if (lane == 0) {
+      umma::mbar_arrive_expect_tx(&full, (uint32_t)((with_state ? DK * CT * 4 : 0) +
+                                                    acc * (DK + CT) * 4 + 2 * T * DK * 4 + cbytes +
+                                                    T * CT * es));
     }
-    for (int i = tid; i < acc * DK / 4; i += DR_THREADS) reinterpret_cast<float4*>(rk_s)[i] = rk[i];
-    for (int i = tid; i < acc * (DR_TILE / 4); i += DR_THREADS)
-      reinterpret_cast<float4*>(u_s)[i] =
-          *reinterpret_cast<const float4*>(recu + (int64_t)(i >> 3) * d_v + (i & 7) * 4);
-    const float4* cg = reinterpret_cast<const float4*>(
-        reinterpret_cast<const float*>(ws + p.ws_coef) + ((int64_t)n * p.H_v + h) * DR_COEF);
-    for (int i = tid; i < DR_COEF / 4; i += DR_THREADS) reinterpret_cast<float4*>(cf)[i] = cg[i];
-  }
-  __syncthreads();
-
-  // ---- commit
-  if (acc > 0) {
-    const float w0 = cf[DR_W0];
-#pragma unroll
-    for (int m = 0; m < RPT; ++m) {
-      s[m].x *= w0; s[m].y *= w0; s[m].z *= w0; s[m].w *= w0;
-    }
-    for (int j = 0; j < acc; ++j) {
-      const float w = cf[DR_W + j];
-      float4 u = *reinterpret_cast<const float4*>(u_s + j * DR_TILE + cq * 4);
-      u.x *= w; u.y *= w; u.z *= w; u.w *= w;
-      const float* kr = rk_s + j * DK + rg * RPT;
-      float kv[RPT];
-#pragma unroll
-      for (int m = 0; m < RPT; m += 2) {
-        const float2 k2 = *reinterpret_cast<const float2*>(kr + m);
-        kv[m] = k2.x; kv[m + 1] = k2.y;
-      }
-#pragma unroll
-      for (int m = 0; m < RPT; ++m) {
-        s[m].x = fmaf(kv[m], u.x, s[m].x);
-        s[m].y = fmaf(kv[m], u.y, s[m].y);
-        s[m].z = fmaf(kv[m], u.z, s[m].z);
-        s[m].w = fmaf(kv[m], u.w, s[m].w);
-      }
-    }
-  }
-  if (acc > 0 || rst) {
-#pragma unroll
-    for (int m = 0; m < RPT; ++m) st4_stream(S + (int64_t)m * d_v, s[m]);
-  }
-  if (T == 0) return;
-
-  // ---- column sums S^T k_t and S^T q_t, four tokens at a time
-  for (int tb = 0; tb < T; tb += 4) {
-    float acc8[8][4];
-#pragma unroll
-    for (int v = 0; v < 8; ++v) {
-      const int t = tb + (v & 3);
-      const float* vr = qk_s + ((v >> 2) * D + (t < T ? t : tb)) * DK + rg * RPT;
-      float kv[RPT];
-#pragma unroll
-      for (int m = 0; m < RPT; m += 2) {
-        const float2 k2 = *reinterpret_cast<const float2*>(vr + m);
-        kv[m] = k2.x; kv[m + 1] = k2.y;
-      }
-      float2 a = make_float2(0.f, 0.f), b = a;
-#pragma unroll
-      for (int m = 0; m < RPT; ++m) {
-        const float2 kk = make_float2(kv[m], kv[m]);
-        a = fma2(make_float2(s[m].x, s[m].y), kk, a);
-        b = fma2(make_float2(s[m].z, s[m].w), kk, b);
-      }
-      acc8[v][0] = a.x; acc8[v][1] = a.y; acc8[v][2] = b.x; acc8[v][3] = b.y;
-    }
-    // lanes l, l^8, l^16, l^24 share a column quad: halve the vectors at each exchange, so that
-    // each lane ends with two of the eight
-    const bool hi16 = lane & 16, hi8 = lane & 8;
-    float a4[4][4], a2[2][4];
-#pragma unroll
-    for (int v = 0; v < 4; ++v)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float keep = hi16 ? acc8[v + 4][i] : acc8[v][i];
-        const float send = hi16 ? acc8[v][i] : acc8[v + 4][i];
-        a4[v][i] = keep + __shfl_xor_sync(0xffffffffu, send, 16);
-      }
-#pragma unroll
-    for (int v = 0; v < 2; ++v)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float keep = hi8 ? a4[v + 2][i] : a4[v][i];
-        const float send = hi8 ? a4[v][i] : a4[v + 2][i];
-        a2[v][i] = keep + __shfl_xor_sync(0xffffffffu, send, 8);
-      }
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const int row = (hi16 ? D4 : 0) + tb + (hi8 ? 2 : 0) + v;
-      *reinterpret_cast<float4*>(red + ((warp * 2 * D4) + row) * DR_TILE + cq * 4) =
-          make_float4(a2[v][0], a2[v][1], a2[v][2], a2[v][3]);
-    }
-  }
-  __syncthreads();
-
-  // ---- per column (lane): the triangular solve for u (every warp), o of tokens warp, warp + 4, ..
-  auto col_sum = [&](int row) {
-    float x = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) x += red[(w * 2 * D4 + row) * DR_TILE + lane];
-    return x;
+    __syncwarp();
+    const int hk = khead_of(w.h, p.H_k, p.H_v, p.layout);
+    const int64_t nk = (int64_t)w.n * p.H_k + hk;
+    if (lane == 0 && with_state)
+      umma::tma_load_3d(st_s, &tm_state, w.ct * CT, 0, w.hd.slot * p.H_v + w.h, &full);
+    if (lane == 1 && acc > 0)
+      umma::bulk_g2s(rk_s, reinterpret_cast<const float*>(ws + p.ws_rk) + nk * D * DK, acc * DK * 4,
+                     &full);
+    if (lane == 2 && T > 0)
+      umma::bulk_g2s(qk, reinterpret_cast<const float*>(ws + p.ws_qk) + nk * 2 * D * DK,
+                     2 * T * DK * 4, &full);
+    if (lane == 3)
+      umma::bulk_g2s(cf, reinterpret_cast<const float*>(ws + p.ws_coef) +
+                             ((int64_t)w.n * p.H_v + w.h) * DR_COEF, cbytes, &full);
+    if (lane < acc)
+      umma::bulk_g2s(uo_s + lane * CT,
+                     p.rec.u + (((int64_t)w.hd.slot * p.H_v + w.h) * D + lane) * d_v + w.ct * CT,
+                     CT * 4, &full);
+    if (lane >= 16 && lane - 16 < T)
+      umma::bulk_g2s(vs + (lane - 16) * CT * es,
+                     static_cast<const uint8_t*>(p.v) +
+                         (((int64_t)(w.hd.c0 + lane - 16) * p.H_v + w.h) * d_v + w.ct * CT) * es,
+                     CT * es, &full);
   };
-  const int64_t c0 = cu_at(p.cu_seqlens, n);
-  const TV* vg = static_cast<const TV*>(p.v) + (c0 * p.H_v + h) * d_v + tile * DR_TILE + lane;
-  TO* og = static_cast<TO*>(p.o) + (c0 * p.H_v + h) * d_v + tile * DR_TILE + lane;
-  const int64_t tok = (int64_t)p.H_v * d_v;
-  float u[DR_MAX];
-#pragma unroll
-  for (int i = 0; i < DR_MAX; ++i) {
-    u[i] = 0.f;
-    if (i < T) u[i] = cf[DR_BETA + i] * (ld(vg + i * tok) - cf[DR_C + i] * col_sum(i));
+
+  // ---- the first tile's state, before the first kernel's decision on its sequence is known (the
+  // state was written before that kernel started)
+  unsigned t = blockIdx.x;
+  if (tid == 0) {
+    umma::mbar_init(&full, 1);
+    umma::fence_mbar_init();
   }
-#pragma unroll
-  for (int j = 0; j < DR_MAX; ++j) {
-    if (j < T) {
-#pragma unroll
-      for (int i = j + 1; i < DR_MAX; ++i)
-        if (i < T) u[i] = fmaf(-cf[DR_L + j * DR_MAX + i], u[j], u[i]);
+  if (warp == 0) {
+    __syncwarp();
+    DraftTile w = tile_at(p, t, tiles_c);
+    const int slot = p.slot_ids[w.n];
+    const bool rst = p.reset != nullptr && p.reset[w.n] != 0;
+    const bool idle = cu_at(p.cu_seqlens, w.n + 1) == cu_at(p.cu_seqlens, w.n) &&
+                      (!p.accepted || p.accepted[w.n] == 0);
+    const bool early = slot >= 0 && slot < p.n_slots && !rst && !idle;
+    if (early && lane == 0) {
+      umma::mbar_expect_tx(&full, DK * CT * 4);
+      umma::tma_load_3d(st_s, &tm_state, w.ct * CT, 0, slot * p.H_v + w.h, &full);
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // what the first kernel wrote is read by bulk copies too
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    w.hd = header_at(p, w.n);
+    w.loaded = early || tile_works(w.hd);
+    if (tile_works(w.hd)) load_tile(w, 0, !early && !w.hd.rst);
+    else if (early && lane == 0) umma::mbar_arrive(&full);
+    if (lane == 0) tiles[0] = w;
+  } else {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
   }
+  __syncthreads();
+
+  uint32_t phase = 0;
+  for (int it = 0;; ++it, t += gridDim.x) {
+    const bool more = t + gridDim.x < total;
+    if (more && warp == 0) {
+      DraftTile w = tile_at(p, t + gridDim.x, tiles_c);
+      w.hd = header_at(p, w.n);
+      w.loaded = tile_works(w.hd);
+      if (lane == 0) tiles[(it + 1) & 1] = w;
+    }
+    const DraftTile& cur = tiles[it & 1];
+    const int T = cur.hd.len, acc = cur.hd.acc;
+    const bool rst = cur.hd.rst != 0, works = tile_works(cur.hd);
+    float* qk_s = late + (it & 1) * late_sz;
+    const float* cf = qk_s + 2 * D * DK;
+    const int TT = token_pad(T);
+    const float* cL = cf;                   // [TT][TT]: Lt[j][i]
+    const float* cP = cL + TT * TT;         // [TT][TT]: P[i][j]
+    const float* cC = cP + TT * TT;
+    const float* cB = cC + TT;
+    const float* cW = cB + TT;              // commit weights, then that of the old state
+    float4 s[RPT];
+    if (cur.loaded) {
+      if (!umma::mbar_wait(&full, phase, nullptr)) {
+        // the copies never came: give them as long again before the block's memory goes away
+        umma::mbar_wait(&full, phase, nullptr);
+        set_status(p.status, GDN_ETIMEOUT);
+        return;
+      }
+      phase ^= 1;
+    }
+    if (cur.hd.run && tid == 0 && cur.h == 0 && cur.ct == 0) p.rec.n[cur.hd.slot] = T;
+    if (works) {
 #pragma unroll
-  for (int i = 0; i < DR_MAX; ++i)
-    if (i < T && (i & 3) == warp) recu[(int64_t)i * d_v + lane] = u[i];
-  for (int i = warp; i < T; i += 4) {
-    float o = cf[DR_C + i] * col_sum(D4 + i);
+      for (int m = 0; m < RPT; ++m)
+        s[m] = rst ? make_float4(0.f, 0.f, 0.f, 0.f)
+                   : *reinterpret_cast<const float4*>(st_s + (row0 + m) * CT + cq * 4);
+      // ---- commit
+      if (acc > 0) {
+        const float2 w0 = make_float2(cW[DR_MAX], cW[DR_MAX]);
 #pragma unroll
-    for (int j = 0; j < DR_MAX; ++j)
-      if (j <= i) o = fmaf(cf[DR_P + i * DR_MAX + j], u[j], o);
-    st(og + i * tok, o);
+        for (int m = 0; m < RPT; ++m) {
+          const float2 x = mul2(make_float2(s[m].x, s[m].y), w0);
+          const float2 y = mul2(make_float2(s[m].z, s[m].w), w0);
+          s[m] = make_float4(x.x, x.y, y.x, y.y);
+        }
+#pragma unroll 1
+        for (int j = 0; j < acc; ++j) {
+          const float w = cW[j];
+          const float4 u = *reinterpret_cast<const float4*>(uo_s + j * CT + cq * 4);
+          const float2 ua = make_float2(u.x * w, u.y * w), ub = make_float2(u.z * w, u.w * w);
+          float kv[RPT];
+          load_rows<RPT>(kv, rk_s + j * DK + row0);
+#pragma unroll
+          for (int m = 0; m < RPT; ++m) {
+            const float2 kk = make_float2(kv[m], kv[m]);
+            const float2 x = fma2(kk, ua, make_float2(s[m].x, s[m].y));
+            const float2 y = fma2(kk, ub, make_float2(s[m].z, s[m].w));
+            s[m] = make_float4(x.x, x.y, y.x, y.y);
+          }
+        }
+      }
+    }
+    __syncthreads();  // the state, the old record and the sums of the tile before have been read
+    if (more && warp == 0) {
+      const DraftTile& w = tiles[(it + 1) & 1];
+      if (w.loaded) load_tile(w, (it + 1) & 1, !w.hd.rst);
+    }
+    if (works && (acc > 0 || rst)) {
+      float* S = p.state + (((int64_t)cur.hd.slot * p.H_v + cur.h) * DK + row0) * d_v +
+                 cur.ct * CT + cq * 4;
+#pragma unroll
+      for (int m = 0; m < RPT; ++m) st4_stream(S + (int64_t)m * d_v, s[m]);
+    }
+    if (works && T > 0) {
+      const int team = tid / CT, col = tid % CT;
+      float u[MAXT], qs[MAXT / TEAMS];
+#pragma unroll
+      for (int g = 0; g < MAXT / G; ++g) {
+        if (g * G < T) {
+          if (g > 0) __syncthreads();  // the sums of the tokens before have been read
+          const int cnt = T - g * G < G ? T - g * G : G;
+          // ---- column sums S^T k_t and S^T q_t, NRW tokens at a time
+#pragma unroll 1
+          for (int kind = 0; kind < 2; ++kind)
+#pragma unroll 1
+            for (int tb = 0; tb < cnt; tb += NRW) {
+              const float* vr = qk_s + (kind * T + g * G + tb) * DK + row0;
+              float x[NRW][4];
+#pragma unroll
+              for (int v = 0; v < NRW; v += 2) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) x[v][c] = x[v + 1][c] = 0.f;
+#pragma unroll
+                for (int m = 0; m < RPT; m += 4) {
+                  float k0[4], k1[4];
+                  load_rows<(RPT < 4 ? RPT : 4)>(k0, vr + v * DK + m);
+                  load_rows<(RPT < 4 ? RPT : 4)>(k1, vr + (v + 1) * DK + m);
+#pragma unroll
+                  for (int i = 0; i < 4 && m + i < RPT; ++i) {
+                    fma_row(x[v], s[m + i], k0[i]);
+                    fma_row(x[v + 1], s[m + i], k1[i]);
+                  }
+                }
+              }
+              // the NRW row groups of a warp share a column quad: halve the tokens at each
+              // exchange, so that a lane ends with one of them
+              int mine = 0;
+#pragma unroll
+              for (int half = NRW / 2, step = 16; half > 0; half /= 2, step /= 2) {
+                const bool hi = lane & step;
+#pragma unroll
+                for (int v = 0; v < half; ++v)
+#pragma unroll
+                  for (int c = 0; c < 4; ++c) {
+                    const float keep = hi ? x[v + half][c] : x[v][c];
+                    const float send = hi ? x[v][c] : x[v + half][c];
+                    x[v][c] = keep + __shfl_xor_sync(0xffffffffu, send, step);
+                  }
+                mine += hi ? half : 0;
+              }
+              *reinterpret_cast<float4*>(red + ((warp * 2 + kind) * G + tb + mine) * CT + cq * 4) =
+                  make_float4(x[0][0], x[0][1], x[0][2], x[0][3]);
+            }
+          __syncthreads();
+          // ---- per column: the right-hand sides of u (every team), the q sums of the team's tokens
+          auto col_sum = [&](int kind, int r) {
+            float y = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) y += red[((w * 2 + kind) * G + r) * CT + col];
+            return y;
+          };
+          const uint8_t* vs = reinterpret_cast<const uint8_t*>(cf + coef_size(D));
+#pragma unroll
+          for (int r = 0; r < G; ++r) {
+            const int i = g * G + r;
+            u[i] = 0.f;
+            if (i < T) {
+              const int at = i * CT + col;
+              const float v = p.qkv_dtype == GDN_F32    ? reinterpret_cast<const float*>(vs)[at]
+                              : p.qkv_dtype == GDN_BF16 ? ld(reinterpret_cast<const __nv_bfloat16*>(vs) + at)
+                                                        : ld(reinterpret_cast<const __half*>(vs) + at);
+              u[i] = cB[i] * (v - cC[i] * col_sum(0, r));
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < G / TEAMS; ++r) {
+            const int i = r * TEAMS + team;
+            if (g * G + i < T) qs[g * (G / TEAMS) + r] = col_sum(1, i);
+          }
+        }
+      }
+      float* recu = p.rec.u + ((int64_t)cur.hd.slot * p.H_v + cur.h) * D * d_v + cur.ct * CT + col;
+      const int64_t tok = (int64_t)p.H_v * d_v;
+      const int64_t o0 = ((int64_t)cur.hd.c0 * p.H_v + cur.h) * d_v + cur.ct * CT + col;
+      auto finish = [&](auto tt) {
+        constexpr int N = decltype(tt)::value;
+        // the triangular solve; rows of the tables at and behind T are zero
+#pragma unroll
+        for (int j = 0; j < N - 1; ++j)
+#pragma unroll
+          for (int i4 = (j + 1) / 4; i4 < N / 4; ++i4) {
+            const float4 l = *reinterpret_cast<const float4*>(cL + j * N + 4 * i4);
+            if (4 * i4 > j) u[4 * i4] = fmaf(-l.x, u[j], u[4 * i4]);
+            if (4 * i4 + 1 > j) u[4 * i4 + 1] = fmaf(-l.y, u[j], u[4 * i4 + 1]);
+            if (4 * i4 + 2 > j) u[4 * i4 + 2] = fmaf(-l.z, u[j], u[4 * i4 + 2]);
+            u[4 * i4 + 3] = fmaf(-l.w, u[j], u[4 * i4 + 3]);
+          }
+#pragma unroll
+        for (int r = 0; r < N / TEAMS; ++r) {
+          const int i = r * TEAMS + team;
+          if (i < T) {
+            float ui = u[r * TEAMS];
+#pragma unroll
+            for (int m = 1; m < TEAMS; ++m) ui = team == m ? u[r * TEAMS + m] : ui;
+            recu[(int64_t)i * d_v] = ui;
+            float o = cC[i] * qs[r];
+#pragma unroll
+            for (int j4 = 0; 4 * j4 <= r * TEAMS + TEAMS - 1; ++j4) {
+              const float4 c = *reinterpret_cast<const float4*>(cP + i * N + 4 * j4);
+              o = fmaf(c.x, u[4 * j4], o);
+              o = fmaf(c.y, u[4 * j4 + 1], o);
+              o = fmaf(c.z, u[4 * j4 + 2], o);
+              o = fmaf(c.w, u[4 * j4 + 3], o);
+            }
+            if (p.o_dtype == GDN_F32) static_cast<float*>(p.o)[o0 + i * tok] = o;
+            else st(static_cast<__nv_bfloat16*>(p.o) + o0 + i * tok, o);
+          }
+        }
+      };
+      if (TT == 4) finish(std::integral_constant<int, 4>{});
+      else if (MAXT == 8 || TT == 8) finish(std::integral_constant<int, 8>{});
+      else finish(std::integral_constant<int, MAXT>{});
+    }
+    if (!more) return;
   }
 }
 
@@ -548,9 +731,9 @@ __global__ void __launch_bounds__(256) draft_gate_kernel(const DraftArgs p, cons
 int prep_smem(int d_k, int r) {
   return (2 * DR_MAX * (d_k + 4) + 4 * 2 * DR_MAX * DR_MAX + 3 * r * DR_MAX) * 4;
 }
-int state_smem(int d_k, int depth) {
-  const int d4 = (depth + 3) & ~3;
-  return (3 * depth * d_k + depth * DR_TILE + 8 * d4 * DR_TILE + DR_COEF) * 4;
+int state_smem(int d_k, int ct, int max_t, int depth, int es) {
+  return (d_k * ct + depth * (d_k + ct) + 2 * late_floats(d_k, ct, depth, es) +
+          8 * (max_t / 2) * ct) * 4;
 }
 
 template <int DK, typename TX, typename TS, bool FUSED>
@@ -583,33 +766,56 @@ cudaError_t launch_prep_k(const DraftArgs& a, cudaStream_t s) {
   return cudaErrorInvalidValue;
 }
 
-template <int DK, typename TV, typename TO>
-cudaError_t launch_state(const DraftArgs& a0, cudaStream_t s) {
-  auto kern = draft_state_kernel<DK, TV, TO>;
-  DraftArgs a = a0;
-  const int bytes = state_smem(DK, a.rec.depth);
-  if (bytes > 48 * 1024) {
-    static std::atomic<int> smem_set[64];
-    const cudaError_t e = allow_smem(kern, bytes, smem_set);
-    if (e != cudaSuccess) return e;
-  }
+// The state pool as [heads of all slots][d_k][d_v] fp32, a box of d_k rows x ct columns.
+cudaError_t state_map(CUtensorMap* m, const DraftArgs& a, int ct) {
+  const TensorMapEncodeFn enc = tensor_map_encode();
+  if (!enc) return cudaErrorNotSupported;
+  const int64_t heads = (int64_t)a.n_slots * a.H_v;
+  if (heads > 0x7fffffff) return cudaErrorInvalidValue;
+  const cuuint64_t dims[3] = {(cuuint64_t)a.d_v, (cuuint64_t)a.d_k, (cuuint64_t)heads};
+  const cuuint64_t strides[2] = {(cuuint64_t)a.d_v * 4, (cuuint64_t)a.d_k * a.d_v * 4};
+  const cuuint32_t box[3] = {(cuuint32_t)ct, (cuuint32_t)a.d_k, 1}, estr[3] = {1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, a.state, dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int DK, int CT, int MAXT>
+cudaError_t launch_state(const DraftArgs& a, cudaStream_t s) {
+  auto kern = draft_state_kernel<DK, CT, MAXT>;
+  alignas(64) CUtensorMap tm;
+  cudaError_t e = state_map(&tm, a, CT);
+  if (e != cudaSuccess) return e;
+  const int es = a.qkv_dtype == GDN_F32 ? 4 : 2;
+  const int bytes = state_smem(DK, CT, MAXT, a.rec.depth, es);
+  static std::atomic<int> smem_set[64];
+  // for the largest depth, so that the limit is set once
+  e = allow_smem(kern, state_smem(DK, CT, MAXT, MAXT, 4), smem_set);
+  if (e != cudaSuccess) return e;
+  const int sms = sm_count();
+  if (sms == 0) return cudaErrorInvalidDevice;
+  // as many blocks as fit at once: 228 KB of shared memory per SM, 1 KB of it per block reserved
+  int per_sm = 228 * 1024 / (bytes + 1024 + 128);
+  if (per_sm > (MAXT <= 8 ? 4 : 2)) per_sm = MAXT <= 8 ? 3 : 2;
+  const int64_t total = (int64_t)a.n_seqs * a.H_v * (a.d_v / CT);
+  if (total > 0x7fffffff) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.d_v / DR_TILE, a.H_v, a.n_seqs);
+  cfg.gridDim = dim3((unsigned)(total < (int64_t)sms * per_sm ? total : (int64_t)sms * per_sm));
   cfg.blockDim = dim3(DR_THREADS);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  return cudaLaunchKernelEx(&cfg, kern, a, tm);
 }
 
-template <int DK, typename TV>
-cudaError_t launch_state_o(const DraftArgs& a, cudaStream_t s) {
-  return a.o_dtype == GDN_BF16 ? launch_state<DK, TV, __nv_bfloat16>(a, s)
-                               : launch_state<DK, TV, float>(a, s);
+template <int DK, int CT>
+cudaError_t launch_state_t(const DraftArgs& a, cudaStream_t s) {
+  return a.rec.depth <= 8 ? launch_state<DK, CT, 8>(a, s) : launch_state<DK, CT, DR_MAX>(a, s);
 }
 
 template <int VPL, typename TZ, typename TO>
@@ -645,12 +851,7 @@ cudaError_t launch_both(const DraftArgs& a0, cudaStream_t s) {
     a.v = static_cast<uint8_t*>(a.workspace) + a.ws_v;
     a.qkv_dtype = GDN_F32;
   }
-  switch (a.qkv_dtype) {
-    case GDN_F32: return launch_state_o<DK, float>(a, s);
-    case GDN_BF16: return launch_state_o<DK, __nv_bfloat16>(a, s);
-    case GDN_F16: return launch_state_o<DK, __half>(a, s);
-  }
-  return cudaErrorInvalidValue;
+  return a.d_v % 64 == 0 ? launch_state_t<DK, 64>(a, s) : launch_state_t<DK, 32>(a, s);
 }
 
 }  // namespace

@@ -100,9 +100,8 @@ struct DraftArgs {
   int H_k, H_v, d_k, d_v, d_conv, n_slots;
   int layout;
   int32_t* status;
-  // set by the launcher: byte offsets of the workspace's parts, L2 prefetch distance in blocks
+  // set by the launcher: byte offsets of the workspace's parts
   size_t ws_hdr, ws_qk, ws_rk, ws_coef, ws_v;
-  int pf_dist;
 };
 
 // out[m][n] = act(sum_k x[m][k] w[n][k] + bias[n]) + residual[m][n]; strides in elements.

@@ -17,8 +17,6 @@
 // atomics).
 #include <cuda.h>
 
-#include <mutex>
-
 #include "gdn_common.cuh"
 #include "gdn_internal.h"
 #include "umma.cuh"
@@ -627,27 +625,10 @@ linear_pair_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
 }
 
 // ------------------------------------------------------------------------------- host side
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeFn linear_encode() {
-  static EncodeFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) ==
-            cudaSuccess && q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeFn>(f);
-  });
-  return fn;
-}
-
 // 16-bit [rows][K] with a row stride of ld elements; box = 64 K elements x `box_rows` rows.
 cudaError_t make_map(CUtensorMap* m, const void* base, bool bf16, int64_t rows, int K, int64_t ld,
                      int box_rows) {
-  EncodeFn enc = linear_encode();
+  const TensorMapEncodeFn enc = tensor_map_encode();
   if (!enc) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};

@@ -1467,27 +1467,9 @@ size_t prefill_tc_workspace(int H_v, int d_k, int d_v, int64_t T_total, int n_se
 }
 
 namespace {
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) ==
-            cudaSuccess && q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(f);
-  });
-  return fn;
-}
-
 // fp16 [T][H][128] viewed as a 3-D tensor (128, H, T); box = one head's 64 consecutive tokens.
 cudaError_t make_head_map(CUtensorMap* m, const void* base, int H, int64_t T) {
-  EncodeTiledFn enc = encode_fn();
+  const TensorMapEncodeFn enc = tensor_map_encode();
   if (!enc) return cudaErrorNotSupported;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)(T > 0 ? T : 1)};
   const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2};
@@ -1501,7 +1483,7 @@ cudaError_t make_head_map(CUtensorMap* m, const void* base, int H, int64_t T) {
 }
 // bf16 x [T][conv_dim] as a 2-D tensor (conv_dim, T); box = 128 channels x (64 + 3) rows.
 cudaError_t make_x_map(CUtensorMap* m, const void* base, int cdim, int64_t T) {
-  EncodeTiledFn enc = encode_fn();
+  const TensorMapEncodeFn enc = tensor_map_encode();
   if (!enc) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {(cuuint64_t)cdim, (cuuint64_t)(T > 0 ? T : 1)};
   const cuuint64_t strides[1] = {(cuuint64_t)cdim * 2};
