@@ -57,6 +57,10 @@ __host__ __device__ __forceinline__ int coef_size(int T) {
 }
 constexpr int DR_COEF = 2 * DR_MAX * DR_MAX + 3 * DR_MAX + 4;  // coef_size(DR_MAX)
 
+// Bytes of state that the first kernel asks L2 for ahead of the second: about what HBM delivers
+// while it runs.
+constexpr int64_t kStateAhead = 32 << 20;
+
 // A set of the state kernel's second inputs in shared memory (es: bytes of a v element), in floats.
 __host__ __device__ __forceinline__ int late_floats(int d_k, int ct, int depth, int es) {
   return 2 * depth * d_k + coef_size(depth) + depth * ct * es / 4;
@@ -81,10 +85,12 @@ __device__ __forceinline__ void fma_row(float* x, const float4& s, float k) {
   x[3] = fmaf(s.w, k, x[3]);
 }
 
-// N consecutive floats (N a multiple of 2, rows of a key's share) from shared memory.
+// N consecutive floats (N a power of two) from shared memory.
 template <int N>
 __device__ __forceinline__ void load_rows(float* x, const float* from) {
-  if constexpr (N == 2) {
+  if constexpr (N == 1) {
+    x[0] = from[0];
+  } else if constexpr (N == 2) {
     const float2 a = *reinterpret_cast<const float2*>(from);
     x[0] = a.x; x[1] = a.y;
   } else {
@@ -150,79 +156,104 @@ __device__ __forceinline__ void token_dots(const float* vec, float* part) {
   for (int a = 0; a < BS; ++a)
 #pragma unroll
     for (int b = 0; b < BS; ++b)
-      part[(warp * 2 * DR_MAX + ib + 8 * a) * DR_MAX + jb + 4 * b] = acc[a][b];
+      part[(warp * 8 * BS + ib + 8 * a) * 4 * BS + jb + 4 * b] = acc[a][b];
 }
 
 // TX: q, k (given) or x; TS: conv state. FUSED: from raw x.
 template <int DK, typename TX, typename TS, bool FUSED>
-__global__ void __launch_bounds__(DR_THREADS) draft_prep_kernel(const DraftArgs p) {
+__global__ void __launch_bounds__(DR_THREADS, FUSED ? 4 : 7) draft_prep_kernel(const DraftArgs p) {
   constexpr int LDV = DK + 4, LPH = DK / 4;
   extern __shared__ __align__(128) float sm[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hk = blockIdx.x, n = blockIdx.y;
   const int r = p.H_v / p.H_k, D = p.rec.depth;
   const bool lead = tid == 0 && hk == 0;
+  // the kernels before have ended when the second kernel's blocks start
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   uint8_t* ws = static_cast<uint8_t*>(p.workspace);
   DraftHeader* hdr = reinterpret_cast<DraftHeader*>(ws + p.ws_hdr) + n;
 
-  // ---- validity (the same decision in every block of the sequence)
+  // ---- validity (the same decision in every block of the sequence); what needs one more load,
+  // the record's count, and the earlier slot ids are looked at while the inputs are on their way
   const int64_t c0 = cu_at(p.cu_seqlens, n), c1 = cu_at(p.cu_seqlens, n + 1);
   const int slot = p.slot_ids[n];
   const bool rst = p.reset != nullptr && p.reset[n] != 0;
-  const int acc = (rst || !p.accepted) ? 0 : p.accepted[n];
+  const int acc_in = (rst || !p.accepted) ? 0 : p.accepted[n];
   int err = 0;
   if (c0 < 0 || c1 < c0 || c1 > p.T_total || c1 - c0 > D) err = GDN_EINVAL;
   else if (slot < 0 || slot >= p.n_slots) err = GDN_ESLOT;
-  if (block_slot_taken(p.slot_ids, n, slot) && err == 0) err = GDN_ESLOT;
-  if (err == 0 && acc != 0 && (acc < 0 || acc > D || acc > p.rec.n[slot])) err = GDN_EINVAL;
-  if (err != 0) {
-    if (lead) {
-      set_status(p.status, err);
-      *hdr = DraftHeader{};
-    }
-    return;
+  const bool known = err == 0 && acc_in >= 0 && acc_in <= D;
+  const int T = known ? (int)(c1 - c0) : 0, acc = known ? acc_in : 0;
+  const int most = acc_in != 0 && err == 0 ? p.rec.n[slot] : 0;
+  // The second kernel's state stream starts here: the first blocks of the grid, whose states are
+  // the first to be used, ask L2 for them (kStateAhead).
+  if (tid < r && (T > 0 || acc > 0) && !rst && n * p.H_k + hk < p.pf_blocks) {
+    const int h = (p.layout & GDN_GQA_TILED) ? hk + tid * p.H_k : hk * r + tid;
+    prefetch_l2(p.state + ((int64_t)slot * p.H_v + h) * DK * p.d_v, (uint32_t)(DK * p.d_v * 4));
   }
-  const int T = (int)(c1 - c0);
-  if (lead) *hdr = DraftHeader{1, acc, T, rst ? 1 : 0, slot, (int)c0, 0, 0};
-  const int bs = T <= 4 ? 1 : T <= 8 ? 2 : 4, T4 = 4 * bs;
+  int hit = 0;
+  for (int m = tid; m < n; m += DR_THREADS) hit |= p.slot_ids[m] == slot;
+  // Settles the validity (block-wide): false, and the error on record, for a sequence to skip.
+  auto settle = [&]() {
+    if (__syncthreads_or(hit) && err == 0) err = GDN_ESLOT;
+    if (err == 0 && acc_in != 0 && (acc_in < 0 || acc_in > D || acc_in > most)) err = GDN_EINVAL;
+    if (lead) {
+      if (err != 0) set_status(p.status, err);
+      *hdr = err != 0 ? DraftHeader{} : DraftHeader{1, acc, T, rst ? 1 : 0, slot, (int)c0, 0, 0};
+    }
+    return err == 0;
+  };
+  const int T4 = token_pad(T), TD = token_pad(D);
 
-  float* vec = sm;                        // [2 DR_MAX][LDV]: k rows 0..T4-1, q rows T4..2 T4-1
-  float* part = vec + 2 * DR_MAX * LDV;   // [4][2 DR_MAX][DR_MAX]
-  float* ge = part + 4 * 2 * DR_MAX * DR_MAX;  // [r][DR_MAX] new decays
-  float* gb = ge + r * DR_MAX;            // [r][DR_MAX] new betas
-  float* go = gb + r * DR_MAX;            // [r][DR_MAX] old decays
+  float* vec = sm;                     // [2 T4][LDV]: k rows 0..T4-1, q rows T4..2 T4-1
+  float* part = vec + 2 * TD * LDV;    // [4][2 T4][T4]
+  float* ge = part + 4 * 2 * TD * TD;  // [r][DR_MAX] new decays
+  float* gb = ge + r * DR_MAX;         // [r][DR_MAX] new betas
+  float* go = gb + r * DR_MAX;         // [r][DR_MAX] old decays
 
-  // ---- the accepted keys of the old record, to the workspace; the thread that reads an element
-  // here is the one that overwrites it below
+  if constexpr (!FUSED) {
+    for (int i = tid; i < 2 * T * LPH; i += DR_THREADS) {
+      const int w = i / (T * LPH), t = i / LPH - w * T, d = (i % LPH) * 4;
+      const TX* src = static_cast<const TX*>(w ? p.q : p.k) + ((c0 + t) * p.H_k + hk) * DK + d;
+      *reinterpret_cast<float4*>(vec + (w * T4 + t) * LDV + d) = ld4(src);
+    }
+    if (!settle()) return;
+  }
+
+  // The accepted keys of the old record, to the workspace; the thread that reads an element here is
+  // the one that overwrites it below.
   float* rk = reinterpret_cast<float*>(ws + p.ws_rk) + ((int64_t)n * p.H_k + hk) * D * DK;
   float* reck = p.rec.k + ((int64_t)slot * p.H_k + hk) * D * DK;
-  for (int i = tid; i < acc * LPH; i += DR_THREADS)
-    reinterpret_cast<float4*>(rk)[i] = reinterpret_cast<const float4*>(reck)[i];
-
-  // ---- gates of the key head's value heads, old and new decays
-  for (int i = tid; i < r * DR_MAX; i += DR_THREADS) {
-    const int jv = i / DR_MAX, t = i % DR_MAX;
-    const int h = (p.layout & GDN_GQA_TILED) ? hk + jv * p.H_k : hk * r + jv;
-    float* rece = p.rec.e + ((int64_t)slot * p.H_v + h) * D;
-    if (t < acc) go[i] = rece[t];
-    if (t < T) {
-      float e, b;
-      if constexpr (FUSED) {
-        const float z = gate_alpha(p.fa, c0 + t, h, p.H_k, p.H_v, p.layout) + p.dt_bias[h];
-        e = expf(-expf(p.A_log[h]) * softplusf_(z));
-        b = sigmoidf_(gate_beta_logit(p.fa, p.fb, c0 + t, h, p.H_k, p.H_v, p.layout));
-      } else {
-        e = expf(p.g[(c0 + t) * p.H_v + h]);
-        b = p.beta[(c0 + t) * p.H_v + h];
+  auto keep_keys = [&]() {
+    for (int i = tid; i < acc * LPH; i += DR_THREADS)
+      reinterpret_cast<float4*>(rk)[i] = reinterpret_cast<const float4*>(reck)[i];
+  };
+  // Gates of the key head's value heads, old and new decays.
+  auto gates = [&]() {
+    for (int i = tid; i < r * DR_MAX; i += DR_THREADS) {
+      const int jv = i / DR_MAX, t = i % DR_MAX;
+      const int h = (p.layout & GDN_GQA_TILED) ? hk + jv * p.H_k : hk * r + jv;
+      float* rece = p.rec.e + ((int64_t)slot * p.H_v + h) * D;
+      if (t < acc) go[i] = rece[t];
+      if (t < T) {
+        float e, b;
+        if constexpr (FUSED) {
+          const float z = gate_alpha(p.fa, c0 + t, h, p.H_k, p.H_v, p.layout) + p.dt_bias[h];
+          e = expf(-expf(p.A_log[h]) * softplusf_(z));
+          b = sigmoidf_(gate_beta_logit(p.fa, p.fb, c0 + t, h, p.H_k, p.H_v, p.layout));
+        } else {
+          e = expf(p.g[(c0 + t) * p.H_v + h]);
+          b = p.beta[(c0 + t) * p.H_v + h];
+        }
+        ge[i] = e;
+        gb[i] = b;
+        rece[t] = e;
       }
-      ge[i] = e;
-      gb[i] = b;
-      rece[t] = e;
     }
-  }
+  };
 
-  // ---- q and k of the tokens into shared memory (and v to the workspace, from raw x)
+  // ---- q and k of the tokens into shared memory and v to the workspace, from raw x
   if constexpr (FUSED) {
     const int R = p.d_conv > 0 ? p.d_conv - 1 : 0;
     const int64_t conv_dim = 2LL * p.H_k * DK + (int64_t)p.H_v * p.d_v;
@@ -233,40 +264,59 @@ __global__ void __launch_bounds__(DR_THREADS) draft_prep_kernel(const DraftArgs 
     const int vq = p.d_v / 4;
     // warp 0: q, warp 1: k, warps 2 and 3: the v quads of the r value heads
     const int n_item = warp < 2 ? 1 : (r * vq + 63 - (tid - 64)) / 64;
-    for (int it = 0; it < n_item; ++it) {
-      int64_t ch;
-      bool active;
+    bool settled = false;
+    for (int it = 0; it < n_item || !settled; ++it) {
+      int64_t ch = 0;
+      bool active = it < n_item;
       int jv = 0, qd = 0;
       if (warp < 2) {
-        active = lane < LPH;
-        ch = (int64_t)warp * p.H_k * DK + (int64_t)hk * DK + (active ? lane * 4 : 0);
-      } else {
+        active = active && lane < LPH;
+        if (active) ch = (int64_t)warp * p.H_k * DK + (int64_t)hk * DK + lane * 4;
+      } else if (active) {
         const int item = tid - 64 + it * 64;
-        active = true;
         jv = item / vq; qd = item % vq;
         const int h = (p.layout & GDN_GQA_TILED) ? hk + jv * p.H_k : hk * r + jv;
         ch = 2LL * p.H_k * DK + (int64_t)h * p.d_v + qd * 4;
       }
       // taps right-aligned: wa[.][3] multiplies the current token, wa[.][2 - i] the window
       float wa[4][4], win[3][4];
+      if (p.d_conv == 4) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int tap = p.d_conv - 4 + i;
-          wa[j][i] = (active && tap >= 0) ? p.conv_w[(ch + j) * p.d_conv + tap] : 0.f;
+        for (int j = 0; j < 4; ++j) {
+          const float4 w = active ? ld4(p.conv_w + (ch + j) * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+          wa[j][0] = w.x; wa[j][1] = w.y; wa[j][2] = w.z; wa[j][3] = w.w;
         }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int tap = p.d_conv - 4 + i;
+            wa[j][i] = (active && tap >= 0) ? p.conv_w[(ch + j) * p.d_conv + tap] : 0.f;
+          }
+      }
       // the window behind the accepted tokens: the last R rows of [conv state; recorded x[:acc]]
 #pragma unroll
       for (int sl = 0; sl < 3; ++sl) {
         const int row = sl - (3 - R);  // 0 = oldest
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (active && row >= 0 && !rst) {
+        if (active && row >= 0 && !rst && known) {
           const int at = row + acc;
           v = at < R ? ld4(cst + (int64_t)at * conv_dim + ch)
                      : ld4(recx + (int64_t)(at - R) * conv_dim + ch);
         }
         win[sl][0] = v.x; win[sl][1] = v.y; win[sl][2] = v.z; win[sl][3] = v.w;
+      }
+      float4 xr[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        xr[u] = (active && u < T) ? ld4(xg + (c0 + u) * conv_dim + ch)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+      if (!settled) {
+        settled = true;
+        if (!settle()) return;
+        keep_keys();
+        gates();
       }
       if (active && R > 0 && (acc > 0 || rst)) {
 #pragma unroll
@@ -278,11 +328,6 @@ __global__ void __launch_bounds__(DR_THREADS) draft_prep_kernel(const DraftArgs 
         }
       }
       for (int tb = 0; tb < T; tb += 4) {
-        float4 xr[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          xr[u] = (active && tb + u < T) ? ld4(xg + (c0 + tb + u) * conv_dim + ch)
-                                         : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int t = tb + u;
@@ -306,12 +351,14 @@ __global__ void __launch_bounds__(DR_THREADS) draft_prep_kernel(const DraftArgs 
             win[1][j] = win[2][j];
             win[2][j] = xs[j];
           }
+          // the next four tokens' inputs are asked for as these are used
+          if (active && t + 4 < T) xr[u] = ld4(xg + (c0 + t + 4) * conv_dim + ch);
           if (warp < 2) {
             const float mul = (warp == 0 ? p.q_scale : 1.0f) / sqrtf(warp_sum(ss) + p.eps);
             if (active)
               *reinterpret_cast<float4*>(vec + ((warp == 0 ? T4 : 0) + t) * LDV + lane * 4) =
                   make_float4(y[0] * mul, y[1] * mul, y[2] * mul, y[3] * mul);
-          } else {
+          } else if (active) {
             const int h = (p.layout & GDN_GQA_TILED) ? hk + jv * p.H_k : hk * r + jv;
             *reinterpret_cast<float4*>(vg + ((c0 + t) * p.H_v + h) * p.d_v + qd * 4) =
                 make_float4(y[0], y[1], y[2], y[3]);
@@ -320,11 +367,8 @@ __global__ void __launch_bounds__(DR_THREADS) draft_prep_kernel(const DraftArgs 
       }
     }
   } else {
-    for (int i = tid; i < 2 * T * LPH; i += DR_THREADS) {
-      const int w = i / (T * LPH), t = i / LPH - w * T, d = (i % LPH) * 4;
-      const TX* src = static_cast<const TX*>(w ? p.q : p.k) + ((c0 + t) * p.H_k + hk) * DK + d;
-      *reinterpret_cast<float4*>(vec + (w * T4 + t) * LDV + d) = ld4(src);
-    }
+    keep_keys();
+    gates();
   }
   __syncthreads();
 
@@ -340,8 +384,8 @@ __global__ void __launch_bounds__(DR_THREADS) draft_prep_kernel(const DraftArgs 
   }
 
   // ---- dot products (rows T..T4-1 are never read back), then the coefficient tables
-  if (bs == 1) token_dots<1, DK>(vec, part);
-  else if (bs == 2) token_dots<2, DK>(vec, part);
+  if (T4 == 4) token_dots<1, DK>(vec, part);
+  else if (T4 == 8) token_dots<2, DK>(vec, part);
   else token_dots<4, DK>(vec, part);
   __syncthreads();
   float* coef = reinterpret_cast<float*>(ws + p.ws_coef);
@@ -357,8 +401,8 @@ __global__ void __launch_bounds__(DR_THREADS) draft_prep_kernel(const DraftArgs 
       for (int l = col + 1; l <= row; ++l) d *= ge[jv * DR_MAX + l];
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        kk += part[(w * 2 * DR_MAX + row) * DR_MAX + col];
-        qq += part[(w * 2 * DR_MAX + T4 + row) * DR_MAX + col];
+        kk += part[(w * 2 * T4 + row) * T4 + col];
+        qq += part[(w * 2 * T4 + T4 + row) * T4 + col];
       }
     }
     cP[row * T4 + col] = in ? d * qq : 0.f;
@@ -407,13 +451,22 @@ __device__ __forceinline__ bool tile_works(const DraftHeader& h) {
   return h.run && (h.acc > 0 || h.len > 0 || h.rst);
 }
 
+// Threads of a block of the state kernel and, at most, blocks of it on an SM, for records of up to
+// max_t tokens: 16 warps on an SM either way, but the longer records' inputs leave shared memory
+// for two blocks only.
+__host__ __device__ constexpr int st_threads(int max_t) { return max_t <= 8 ? 128 : 256; }
+__host__ __device__ constexpr int st_blocks(int max_t) { return max_t <= 8 ? 4 : 2; }
+constexpr int ST_GROUP = 4;  // tokens summed between two barriers
+
 template <int DK, int CT, int MAXT>
-__global__ void __launch_bounds__(DR_THREADS, MAXT <= 8 ? 4 : 2)
+__global__ void __launch_bounds__(st_threads(MAXT), st_blocks(MAXT))
     draft_state_kernel(const DraftArgs p, const __grid_constant__ CUtensorMap tm_state) {
-  constexpr int RPT = DK * CT / (4 * DR_THREADS);  // state rows of a thread
-  constexpr int QL = CT / 4, NRW = 32 / QL;        // lanes per row, row groups of a warp
-  constexpr int TEAMS = DR_THREADS / CT;           // threads per column in the solve
-  constexpr int G = MAXT / 2;                      // tokens summed between two barriers
+  constexpr int NT = st_threads(MAXT), NW = NT / 32;
+  constexpr int RPT = DK * CT / (4 * NT);    // state rows of a thread
+  constexpr int QL = CT / 4, NRW = 32 / QL;  // lanes per row, row groups of a warp
+  constexpr int TEAMS = NT / CT;             // threads per column behind the sums
+  constexpr int G = ST_GROUP;
+  static_assert(RPT >= 1 && MAXT % TEAMS == 0, "shape");
   extern __shared__ __align__(128) float sm[];
   __shared__ __align__(8) uint64_t full;
   __shared__ DraftTile tiles[2];  // this tile and the next
@@ -432,7 +485,8 @@ __global__ void __launch_bounds__(DR_THREADS, MAXT <= 8 ? 4 : 2)
   // the last set's queries, all inside this block's memory.
   float* late = uo_s + D * CT;
   const int late_sz = late_floats(DK, CT, D, es);
-  float* red = late + 2 * late_sz;  // [4 warps][k, q][G][CT]
+  float* red = late + 2 * late_sz;   // [warps][k, q][G][CT]
+  float* w_s = red + 2 * NW * G * CT;  // [MAXT][CT] right-hand sides of u
 
   // Loads of a tile, by warp 0: the state (unless the first tile has asked for it already) and
   // the rest of what its sequence needs, all counted on `full`.
@@ -579,11 +633,11 @@ __global__ void __launch_bounds__(DR_THREADS, MAXT <= 8 ? 4 : 2)
     }
     if (works && T > 0) {
       const int team = tid / CT, col = tid % CT;
-      float u[MAXT], qs[MAXT / TEAMS];
+      constexpr int QN = MAXT > TEAMS ? MAXT / TEAMS : 1;
+      float qs[QN];  // q sums of tokens team, team + TEAMS, ..
 #pragma unroll
       for (int g = 0; g < MAXT / G; ++g) {
         if (g * G < T) {
-          if (g > 0) __syncthreads();  // the sums of the tokens before have been read
           const int cnt = T - g * G < G ? T - g * G : G;
           // ---- column sums S^T k_t and S^T q_t, NRW tokens at a time
 #pragma unroll 1
@@ -596,13 +650,14 @@ __global__ void __launch_bounds__(DR_THREADS, MAXT <= 8 ? 4 : 2)
               for (int v = 0; v < NRW; v += 2) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) x[v][c] = x[v + 1][c] = 0.f;
+                constexpr int kStep = RPT < 4 ? RPT : 4;
 #pragma unroll
-                for (int m = 0; m < RPT; m += 4) {
-                  float k0[4], k1[4];
-                  load_rows<(RPT < 4 ? RPT : 4)>(k0, vr + v * DK + m);
-                  load_rows<(RPT < 4 ? RPT : 4)>(k1, vr + (v + 1) * DK + m);
+                for (int m = 0; m < RPT; m += kStep) {
+                  float k0[kStep], k1[kStep];
+                  load_rows<kStep>(k0, vr + v * DK + m);
+                  load_rows<kStep>(k1, vr + (v + 1) * DK + m);
 #pragma unroll
-                  for (int i = 0; i < 4 && m + i < RPT; ++i) {
+                  for (int i = 0; i < kStep; ++i) {
                     fma_row(x[v], s[m + i], k0[i]);
                     fma_row(x[v + 1], s[m + i], k1[i]);
                   }
@@ -628,33 +683,36 @@ __global__ void __launch_bounds__(DR_THREADS, MAXT <= 8 ? 4 : 2)
                   make_float4(x[0][0], x[0][1], x[0][2], x[0][3]);
             }
           __syncthreads();
-          // ---- per column: the right-hand sides of u (every team), the q sums of the team's tokens
+          // ---- per column, a token per team: the right-hand side of u, the q sum
           auto col_sum = [&](int kind, int r) {
             float y = 0.f;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) y += red[((w * 2 + kind) * G + r) * CT + col];
+            for (int w = 0; w < NW; ++w) y += red[((w * 2 + kind) * G + r) * CT + col];
             return y;
           };
           const uint8_t* vs = reinterpret_cast<const uint8_t*>(cf + coef_size(D));
 #pragma unroll
-          for (int r = 0; r < G; ++r) {
-            const int i = g * G + r;
-            u[i] = 0.f;
-            if (i < T) {
+          for (int r0 = 0; r0 < G; r0 += TEAMS) {
+            const int r = r0 + team, i = g * G + r;
+            if (r < G && i < T) {
               const int at = i * CT + col;
               const float v = p.qkv_dtype == GDN_F32    ? reinterpret_cast<const float*>(vs)[at]
                               : p.qkv_dtype == GDN_BF16 ? ld(reinterpret_cast<const __nv_bfloat16*>(vs) + at)
                                                         : ld(reinterpret_cast<const __half*>(vs) + at);
-              u[i] = cB[i] * (v - cC[i] * col_sum(0, r));
+              w_s[at] = cB[i] * (v - cC[i] * col_sum(0, r));
             }
           }
 #pragma unroll
-          for (int r = 0; r < G / TEAMS; ++r) {
-            const int i = r * TEAMS + team;
-            if (g * G + i < T) qs[g * (G / TEAMS) + r] = col_sum(1, i);
+          for (int j = 0; j < QN; ++j) {  // the team's tokens j TEAMS + team that are in this group
+            const int i = j * TEAMS + team, r = i - g * G;
+            if (r >= 0 && r < G && i < T) qs[j] = col_sum(1, r);
           }
+          __syncthreads();  // the sums have been read; the right-hand sides are there
         }
       }
+      float u[MAXT];
+#pragma unroll
+      for (int i = 0; i < MAXT; ++i) u[i] = i < T ? w_s[i * CT + col] : 0.f;
       float* recu = p.rec.u + ((int64_t)cur.hd.slot * p.H_v + cur.h) * D * d_v + cur.ct * CT + col;
       const int64_t tok = (int64_t)p.H_v * d_v;
       const int64_t o0 = ((int64_t)cur.hd.c0 * p.H_v + cur.h) * d_v + cur.ct * CT + col;
@@ -672,16 +730,17 @@ __global__ void __launch_bounds__(DR_THREADS, MAXT <= 8 ? 4 : 2)
             u[4 * i4 + 3] = fmaf(-l.w, u[j], u[4 * i4 + 3]);
           }
 #pragma unroll
-        for (int r = 0; r < N / TEAMS; ++r) {
+        for (int r = 0; r < (N + TEAMS - 1) / TEAMS; ++r) {
           const int i = r * TEAMS + team;
           if (i < T) {
             float ui = u[r * TEAMS];
 #pragma unroll
-            for (int m = 1; m < TEAMS; ++m) ui = team == m ? u[r * TEAMS + m] : ui;
+            for (int m = 1; m < TEAMS && r * TEAMS + m < N; ++m)
+              ui = team == m ? u[r * TEAMS + m] : ui;
             recu[(int64_t)i * d_v] = ui;
             float o = cC[i] * qs[r];
 #pragma unroll
-            for (int j4 = 0; 4 * j4 <= r * TEAMS + TEAMS - 1; ++j4) {
+            for (int j4 = 0; 4 * j4 < N && 4 * j4 <= r * TEAMS + TEAMS - 1; ++j4) {
               const float4 c = *reinterpret_cast<const float4*>(cP + i * N + 4 * j4);
               o = fmaf(c.x, u[4 * j4], o);
               o = fmaf(c.y, u[4 * j4 + 1], o);
@@ -728,25 +787,35 @@ __global__ void __launch_bounds__(256) draft_gate_kernel(const DraftArgs p, cons
     st(out + i, o[i] * inv * g.norm_w[lane * VPL + i] * silu_exact(ld(z + i)));
 }
 
-int prep_smem(int d_k, int r) {
-  return (2 * DR_MAX * (d_k + 4) + 4 * 2 * DR_MAX * DR_MAX + 3 * r * DR_MAX) * 4;
+int prep_smem(int d_k, int r, int depth) {
+  const int td = token_pad(depth);
+  return (2 * td * (d_k + 4) + 4 * 2 * td * td + 3 * r * DR_MAX) * 4;
 }
 int state_smem(int d_k, int ct, int max_t, int depth, int es) {
   return (d_k * ct + depth * (d_k + ct) + 2 * late_floats(d_k, ct, depth, es) +
-          8 * (max_t / 2) * ct) * 4;
+          2 * (st_threads(max_t) / 32) * ST_GROUP * ct + max_t * ct) * 4;
 }
 
 template <int DK, typename TX, typename TS, bool FUSED>
 cudaError_t launch_prep(const DraftArgs& a, cudaStream_t s) {
   auto kern = draft_prep_kernel<DK, TX, TS, FUSED>;
-  const int bytes = prep_smem(DK, a.H_v / a.H_k);
+  const int bytes = prep_smem(DK, a.H_v / a.H_k, a.rec.depth);
   if (bytes > 48 * 1024) {
     static std::atomic<int> smem_set[64];
     const cudaError_t e = allow_smem(kern, bytes, smem_set);
     if (e != cudaSuccess) return e;
   }
-  kern<<<dim3(a.H_k, a.n_seqs), DR_THREADS, bytes, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.H_k, a.n_seqs);
+  cfg.blockDim = dim3(DR_THREADS);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 template <int DK>
@@ -797,7 +866,7 @@ cudaError_t launch_state(const DraftArgs& a, cudaStream_t s) {
   if (sms == 0) return cudaErrorInvalidDevice;
   // as many blocks as fit at once: 228 KB of shared memory per SM, 1 KB of it per block reserved
   int per_sm = 228 * 1024 / (bytes + 1024 + 128);
-  if (per_sm > (MAXT <= 8 ? 4 : 2)) per_sm = MAXT <= 8 ? 3 : 2;
+  if (per_sm > st_blocks(MAXT)) per_sm = st_blocks(MAXT);
   const int64_t total = (int64_t)a.n_seqs * a.H_v * (a.d_v / CT);
   if (total > 0x7fffffff) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[1];
@@ -805,7 +874,7 @@ cudaError_t launch_state(const DraftArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(total < (int64_t)sms * per_sm ? total : (int64_t)sms * per_sm));
-  cfg.blockDim = dim3(DR_THREADS);
+  cfg.blockDim = dim3(st_threads(MAXT));
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;
   cfg.attrs = attr;
@@ -863,6 +932,7 @@ size_t draft_workspace(int H_k, int H_v, int d_k, int d_v, int64_t T_total, int 
 cudaError_t launch_draft(const DraftArgs& a0, const GateArgs* gate, cudaStream_t s) {
   DraftArgs a = a0;
   const DraftWs w = draft_ws(a.H_k, a.H_v, a.d_k, a.d_v, a.T_total, a.n_seqs, a.rec.depth);
+  a.pf_blocks = (int)(kStateAhead / ((int64_t)(a.H_v / a.H_k) * a.d_k * a.d_v * 4));
   a.ws_hdr = w.hdr; a.ws_qk = w.qk; a.ws_rk = w.rk; a.ws_coef = w.coef; a.ws_v = w.v;
   GateArgs g{};
   if (gate) {
