@@ -51,19 +51,16 @@ constexpr int DR_MAX = 16;  // tokens per draft, at most
 // (j <= i), zeros elsewhere; c[TT], beta[TT]; the commit weights of the accepted tokens [DR_MAX]
 // and that of the old state.
 __host__ __device__ __forceinline__ int token_pad(int T) { return T <= 4 ? 4 : T <= 8 ? 8 : 16; }
+__host__ __device__ __forceinline__ int token_groups(int T) { return (T + 3) / 4; }
 __host__ __device__ __forceinline__ int coef_size(int T) {
   const int tt = token_pad(T);
   return 2 * tt * tt + 2 * tt + DR_MAX + 4;
 }
 constexpr int DR_COEF = 2 * DR_MAX * DR_MAX + 3 * DR_MAX + 4;  // coef_size(DR_MAX)
 
-// Bytes of state that the first kernel asks L2 for ahead of the second: about what HBM delivers
-// while it runs.
-constexpr int64_t kStateAhead = 32 << 20;
-
 // A set of the state kernel's second inputs in shared memory (es: bytes of a v element), in floats.
-__host__ __device__ __forceinline__ int late_floats(int d_k, int ct, int depth, int es) {
-  return 2 * depth * d_k + coef_size(depth) + depth * ct * es / 4;
+__host__ __device__ __forceinline__ int late_floats(int ct, int depth, int es) {
+  return token_groups(depth) * ct * es + (coef_size(depth) + 31) / 32 * 32;
 }
 
 // What the first kernel decides about a sequence.
@@ -77,41 +74,35 @@ struct alignas(16) DraftHeader {
   int pad0, pad1;
 };
 
-// x += k s over a quad of columns.
-__device__ __forceinline__ void fma_row(float* x, const float4& s, float k) {
-  x[0] = fmaf(s.x, k, x[0]);
-  x[1] = fmaf(s.y, k, x[1]);
-  x[2] = fmaf(s.z, k, x[2]);
-  x[3] = fmaf(s.w, k, x[3]);
+// What the matrix unit leaves of an fp32 operand: it reads 1 + 8 + 10 bits (tf32) and drops the rest.
+__device__ __forceinline__ float tf32_rest(float x) {
+  return x - __uint_as_float(__float_as_uint(x) & 0xffffe000u);
 }
-
-// N consecutive floats (N a power of two) from shared memory.
-template <int N>
-__device__ __forceinline__ void load_rows(float* x, const float* from) {
-  if constexpr (N == 1) {
-    x[0] = from[0];
-  } else if constexpr (N == 2) {
-    const float2 a = *reinterpret_cast<const float2*>(from);
-    x[0] = a.x; x[1] = a.y;
-  } else {
-#pragma unroll
-    for (int m = 0; m < N; m += 4) {
-      const float4 a = *reinterpret_cast<const float4*>(from + m);
-      x[m] = a.x; x[m + 1] = a.y; x[m + 2] = a.z; x[m + 3] = a.w;
-    }
-  }
+// d += a b: a 16 x 8, b 8 x 8 in tf32, d fp32, in the warp's fragment layout.
+__device__ __forceinline__ void mma_tf32(float (&d)[4], float a0, float a1, float a2, float a3,
+                                         float2 b) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(a2)),
+        "r"(__float_as_uint(a3)), "r"(__float_as_uint(b.x)), "r"(__float_as_uint(b.y)));
 }
+// Keys and queries of a sequence for the matrix instructions, per group of 4 tokens: 8 vectors
+// (4 keys, then 4 queries) in fragment order [d_k / 8][lane]: dimensions 8 step + 2 (lane % 4) and
+// the next, of vector lane / 4.
+__host__ __device__ __forceinline__ int frag_bytes(int d_k, int groups) { return groups * d_k * 32; }
 
 struct DraftWs {
-  size_t hdr, qk, rk, coef, v, o32, total;
+  size_t next, hdr, qk, rk, coef, v, o32, total;
 };
 inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 DraftWs draft_ws(int H_k, int H_v, int d_k, int d_v, int64_t T, int n_seqs, int depth) {
   DraftWs w{};
   const size_t nk = (size_t)n_seqs * H_k, nv = (size_t)n_seqs * H_v;
-  w.hdr = 0;
-  w.qk = up256((size_t)n_seqs * sizeof(DraftHeader));
-  w.rk = w.qk + up256(nk * 2 * depth * d_k * 4);
+  w.next = 0;  // the state kernel's tile counter
+  w.hdr = 256;
+  w.qk = w.hdr + up256((size_t)n_seqs * sizeof(DraftHeader));
+  w.rk = w.qk + up256(nk * frag_bytes(d_k, token_groups(depth)));
   w.coef = w.rk + up256(nk * depth * d_k * 4);
   w.v = w.coef + up256(nv * DR_COEF * 4);
   w.o32 = w.v + up256((size_t)T * H_v * d_v * 4);
@@ -125,7 +116,7 @@ DraftWs draft_ws(int H_k, int H_v, int d_k, int d_v, int64_t T, int n_seqs, int 
 // a load fall into different banks). Partial sums of the 4 warps go to part[warp][row][col].
 template <int BS, int DK>
 __device__ __forceinline__ void token_dots(const float* vec, float* part) {
-  constexpr int LDV = DK + 4, QPW = DK / 16;  // float4 groups per warp
+  constexpr int LDV = DK + 8, QPW = DK / 16;  // float4 groups per warp
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ib = lane >> 2, jb = lane & 3;
   float acc[BS][BS];
@@ -162,8 +153,9 @@ __device__ __forceinline__ void token_dots(const float* vec, float* part) {
 // TX: q, k (given) or x; TS: conv state. FUSED: from raw x.
 template <int DK, typename TX, typename TS, bool FUSED>
 __global__ void __launch_bounds__(DR_THREADS, FUSED ? 4 : 7) draft_prep_kernel(const DraftArgs p) {
-  constexpr int LDV = DK + 4, LPH = DK / 4;
-  extern __shared__ __align__(128) float sm[];
+  constexpr int LDV = DK + 8, LPH = DK / 4;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  float* sm = reinterpret_cast<float*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hk = blockIdx.x, n = blockIdx.y;
   const int r = p.H_v / p.H_k, D = p.rec.depth;
@@ -174,8 +166,9 @@ __global__ void __launch_bounds__(DR_THREADS, FUSED ? 4 : 7) draft_prep_kernel(c
   uint8_t* ws = static_cast<uint8_t*>(p.workspace);
   DraftHeader* hdr = reinterpret_cast<DraftHeader*>(ws + p.ws_hdr) + n;
 
-  // ---- validity (the same decision in every block of the sequence); what needs one more load,
-  // the record's count, and the earlier slot ids are looked at while the inputs are on their way
+  // ---- validity (the same decision in every block of the sequence). What needs one more load,
+  // the record's count, and the earlier slot ids are looked at while the inputs are on their way:
+  // up to the verdict (`settle`) only the workspace is written.
   const int64_t c0 = cu_at(p.cu_seqlens, n), c1 = cu_at(p.cu_seqlens, n + 1);
   const int slot = p.slot_ids[n];
   const bool rst = p.reset != nullptr && p.reset[n] != 0;
@@ -186,12 +179,6 @@ __global__ void __launch_bounds__(DR_THREADS, FUSED ? 4 : 7) draft_prep_kernel(c
   const bool known = err == 0 && acc_in >= 0 && acc_in <= D;
   const int T = known ? (int)(c1 - c0) : 0, acc = known ? acc_in : 0;
   const int most = acc_in != 0 && err == 0 ? p.rec.n[slot] : 0;
-  // The second kernel's state stream starts here: the first blocks of the grid, whose states are
-  // the first to be used, ask L2 for them (kStateAhead).
-  if (tid < r && (T > 0 || acc > 0) && !rst && n * p.H_k + hk < p.pf_blocks) {
-    const int h = (p.layout & GDN_GQA_TILED) ? hk + tid * p.H_k : hk * r + tid;
-    prefetch_l2(p.state + ((int64_t)slot * p.H_v + h) * DK * p.d_v, (uint32_t)(DK * p.d_v * 4));
-  }
   int hit = 0;
   for (int m = tid; m < n; m += DR_THREADS) hit |= p.slot_ids[m] == slot;
   // Settles the validity (block-wide): false, and the error on record, for a sequence to skip.
@@ -200,6 +187,7 @@ __global__ void __launch_bounds__(DR_THREADS, FUSED ? 4 : 7) draft_prep_kernel(c
     if (err == 0 && acc_in != 0 && (acc_in < 0 || acc_in > D || acc_in > most)) err = GDN_EINVAL;
     if (lead) {
       if (err != 0) set_status(p.status, err);
+      if (n == 0) *reinterpret_cast<unsigned*>(ws + p.ws_next) = 0;
       *hdr = err != 0 ? DraftHeader{} : DraftHeader{1, acc, T, rst ? 1 : 0, slot, (int)c0, 0, 0};
     }
     return err == 0;
@@ -212,43 +200,37 @@ __global__ void __launch_bounds__(DR_THREADS, FUSED ? 4 : 7) draft_prep_kernel(c
   float* gb = ge + r * DR_MAX;         // [r][DR_MAX] new betas
   float* go = gb + r * DR_MAX;         // [r][DR_MAX] old decays
 
-  if constexpr (!FUSED) {
-    for (int i = tid; i < 2 * T * LPH; i += DR_THREADS) {
-      const int w = i / (T * LPH), t = i / LPH - w * T, d = (i % LPH) * 4;
-      const TX* src = static_cast<const TX*>(w ? p.q : p.k) + ((c0 + t) * p.H_k + hk) * DK + d;
-      *reinterpret_cast<float4*>(vec + (w * T4 + t) * LDV + d) = ld4(src);
-    }
-    if (!settle()) return;
-  }
-
   // The accepted keys of the old record, to the workspace; the thread that reads an element here is
   // the one that overwrites it below.
   float* rk = reinterpret_cast<float*>(ws + p.ws_rk) + ((int64_t)n * p.H_k + hk) * D * DK;
   float* reck = p.rec.k + ((int64_t)slot * p.H_k + hk) * D * DK;
+  constexpr int KEYS = DR_MAX * LPH / DR_THREADS;
+  float4 old[KEYS];
+#pragma unroll
+  for (int x = 0; x < KEYS; ++x)
+    if (tid + x * DR_THREADS < acc * LPH)
+      old[x] = reinterpret_cast<const float4*>(reck)[tid + x * DR_THREADS];
   auto keep_keys = [&]() {
-    for (int i = tid; i < acc * LPH; i += DR_THREADS)
-      reinterpret_cast<float4*>(rk)[i] = reinterpret_cast<const float4*>(reck)[i];
+#pragma unroll
+    for (int x = 0; x < KEYS; ++x)
+      if (tid + x * DR_THREADS < acc * LPH)
+        reinterpret_cast<float4*>(rk)[tid + x * DR_THREADS] = old[x];
   };
   // Gates of the key head's value heads, old and new decays.
   auto gates = [&]() {
     for (int i = tid; i < r * DR_MAX; i += DR_THREADS) {
       const int jv = i / DR_MAX, t = i % DR_MAX;
       const int h = (p.layout & GDN_GQA_TILED) ? hk + jv * p.H_k : hk * r + jv;
-      float* rece = p.rec.e + ((int64_t)slot * p.H_v + h) * D;
-      if (t < acc) go[i] = rece[t];
+      if (t < acc) go[i] = p.rec.e[((int64_t)slot * p.H_v + h) * D + t];
       if (t < T) {
-        float e, b;
         if constexpr (FUSED) {
           const float z = gate_alpha(p.fa, c0 + t, h, p.H_k, p.H_v, p.layout) + p.dt_bias[h];
-          e = expf(-expf(p.A_log[h]) * softplusf_(z));
-          b = sigmoidf_(gate_beta_logit(p.fa, p.fb, c0 + t, h, p.H_k, p.H_v, p.layout));
+          ge[i] = expf(-expf(p.A_log[h]) * softplusf_(z));
+          gb[i] = sigmoidf_(gate_beta_logit(p.fa, p.fb, c0 + t, h, p.H_k, p.H_v, p.layout));
         } else {
-          e = expf(p.g[(c0 + t) * p.H_v + h]);
-          b = p.beta[(c0 + t) * p.H_v + h];
+          ge[i] = expf(p.g[(c0 + t) * p.H_v + h]);
+          gb[i] = p.beta[(c0 + t) * p.H_v + h];
         }
-        ge[i] = e;
-        gb[i] = b;
-        rece[t] = e;
       }
     }
   };
@@ -314,9 +296,9 @@ __global__ void __launch_bounds__(DR_THREADS, FUSED ? 4 : 7) draft_prep_kernel(c
                                   : make_float4(0.f, 0.f, 0.f, 0.f);
       if (!settled) {
         settled = true;
-        if (!settle()) return;
-        keep_keys();
         gates();
+        keep_keys();
+        if (!settle()) return;
       }
       if (active && R > 0 && (acc > 0 || rst)) {
 #pragma unroll
@@ -366,21 +348,46 @@ __global__ void __launch_bounds__(DR_THREADS, FUSED ? 4 : 7) draft_prep_kernel(c
         }
       }
     }
+    __syncthreads();
   } else {
-    keep_keys();
+    auto from = [&](int i) {
+      const int w = i / (T * LPH), t = i / LPH - w * T, d = (i % LPH) * 4;
+      return ld4(static_cast<const TX*>(w ? p.q : p.k) + ((c0 + t) * p.H_k + hk) * DK + d);
+    };
+    auto put = [&](int i, float4 v) {
+      const int w = i / (T * LPH), t = i / LPH - w * T, d = (i % LPH) * 4;
+      *reinterpret_cast<float4*>(vec + (w * T4 + t) * LDV + d) = v;
+    };
+    float4 in[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      if (tid + x * DR_THREADS < 2 * T * LPH) in[x] = from(tid + x * DR_THREADS);
     gates();
+    keep_keys();
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      if (tid + x * DR_THREADS < 2 * T * LPH) put(tid + x * DR_THREADS, in[x]);
+#pragma unroll 4
+    for (int i = tid + 2 * DR_THREADS; i < 2 * T * LPH; i += DR_THREADS) put(i, from(i));
+    if (!settle()) return;
   }
-  __syncthreads();
 
-  // ---- the new record's keys, and q and k for the state kernel
-  float* qk = reinterpret_cast<float*>(ws + p.ws_qk) + ((int64_t)n * p.H_k + hk) * 2 * D * DK;
-  for (int i = tid; i < T * LPH; i += DR_THREADS) {
-    const int t = i / LPH, d = (i % LPH) * 4;
-    const float4 kv = *reinterpret_cast<const float4*>(vec + t * LDV + d);
-    reinterpret_cast<float4*>(reck)[i] = kv;
-    reinterpret_cast<float4*>(qk)[i] = kv;
-    *reinterpret_cast<float4*>(qk + (int64_t)T * DK + i * 4) =
-        *reinterpret_cast<const float4*>(vec + (T4 + t) * LDV + d);
+  // ---- the new record's decays and keys, and q and k for the state kernel (rows behind the last token of a
+  // group hold anything: what they give is dropped)
+  for (int i = tid; i < r * DR_MAX; i += DR_THREADS) {
+    const int jv = i / DR_MAX, t = i % DR_MAX;
+    const int h = (p.layout & GDN_GQA_TILED) ? hk + jv * p.H_k : hk * r + jv;
+    if (t < T) p.rec.e[((int64_t)slot * p.H_v + h) * D + t] = ge[i];
+  }
+  for (int i = tid; i < T * LPH; i += DR_THREADS)
+    reinterpret_cast<float4*>(reck)[i] =
+        *reinterpret_cast<const float4*>(vec + (i / LPH) * LDV + (i % LPH) * 4);
+  float2* frag = reinterpret_cast<float2*>(ws + p.ws_qk +
+                                           ((int64_t)n * p.H_k + hk) * frag_bytes(DK, token_groups(D)));
+  for (int i = tid; i < token_groups(T) * DK * 4; i += DR_THREADS) {
+    const int step = i >> 5, gr = step / (DK / 8), d = (step % (DK / 8)) * 8 + (lane & 3) * 2;
+    const int v = lane >> 2;
+    frag[i] = *reinterpret_cast<const float2*>(vec + ((v >> 2) * T4 + gr * 4 + (v & 3)) * LDV + d);
   }
 
   // ---- dot products (rows T..T4-1 are never read back), then the coefficient tables
@@ -427,173 +434,216 @@ __global__ void __launch_bounds__(DR_THREADS, FUSED ? 4 : 7) draft_prep_kernel(c
 
 // One (column tile, value head, sequence) of the state kernel's work.
 struct DraftTile {
-  int n, h, ct;  // sequence, value head, column tile
-  bool loaded;   // its copies are under way
   DraftHeader hd;
+  int n, h, ct;  // sequence, value head, column tile
+  int more;      // another one follows
 };
-__device__ __forceinline__ DraftTile tile_at(const DraftArgs& p, unsigned t, int tiles_c) {
-  const unsigned per = (unsigned)(p.H_v * tiles_c);
-  DraftTile w;
-  w.n = (int)(t / per);
-  const unsigned rem = t - (unsigned)w.n * per;
-  w.h = (int)(rem / (unsigned)tiles_c);
-  w.ct = (int)(rem - (unsigned)w.h * (unsigned)tiles_c);
-  return w;
-}
-__device__ __forceinline__ DraftHeader header_at(const DraftArgs& p, int n) {
-  const int4* g = reinterpret_cast<const int4*>(static_cast<const uint8_t*>(p.workspace) + p.ws_hdr) +
-                  2 * (int64_t)n;
-  const int4 a = g[0], b = g[1];
-  return DraftHeader{a.x, a.y, a.z, a.w, b.x, b.y, 0, 0};
-}
 // A sequence without accepted and without new tokens needs no state, unless it starts from zero.
 __device__ __forceinline__ bool tile_works(const DraftHeader& h) {
   return h.run && (h.acc > 0 || h.len > 0 || h.rst);
 }
 
-// Threads of a block of the state kernel and, at most, blocks of it on an SM, for records of up to
-// max_t tokens: 16 warps on an SM either way, but the longer records' inputs leave shared memory
-// for two blocks only.
-__host__ __device__ constexpr int st_threads(int max_t) { return max_t <= 8 ? 128 : 256; }
-__host__ __device__ constexpr int st_blocks(int max_t) { return max_t <= 8 ? 4 : 2; }
-constexpr int ST_GROUP = 4;  // tokens summed between two barriers
+// The state [H_v of all slots][d_v / 32][d_k][32] in boxes of a tile, v and the record's u in boxes
+// of 4 tokens x a tile's columns.
+struct DraftMaps {
+  CUtensorMap state, v, u;
+};
 
-template <int DK, int CT, int MAXT>
+// Shape of the state kernel for records of up to max_t tokens: 16 warps on an SM either way, in
+// blocks as large as what their inputs need of shared memory asks for (64 sequences x 0..16
+// tokens: 107 us with two blocks of 4 warps on an SM).
+__host__ __device__ constexpr int st_threads(int max_t) { return 128; }
+__host__ __device__ constexpr int st_blocks(int max_t) { return max_t <= 4 ? 4 : max_t <= 8 ? 3 : 2; }
+// Columns of a tile; the warps of a block: ct / 32 side by side, st_parts below each other.
+__host__ __device__ constexpr int st_cols(int d_v) { return d_v < 64 ? d_v : 64; }
+__host__ __device__ constexpr int st_parts(int d_k, int d_v, int max_t) {
+  return st_threads(max_t) / 32 / (st_cols(d_v) / 32) < d_k / 16
+             ? st_threads(max_t) / 32 / (st_cols(d_v) / 32)
+             : d_k / 16;
+}
+
+template <int DK, int DV, int MAXT>
 __global__ void __launch_bounds__(st_threads(MAXT), st_blocks(MAXT))
-    draft_state_kernel(const DraftArgs p, const __grid_constant__ CUtensorMap tm_state) {
-  constexpr int NT = st_threads(MAXT), NW = NT / 32;
-  constexpr int RPT = DK * CT / (4 * NT);    // state rows of a thread
-  constexpr int QL = CT / 4, NRW = 32 / QL;  // lanes per row, row groups of a warp
-  constexpr int TEAMS = NT / CT;             // threads per column behind the sums
-  constexpr int G = ST_GROUP;
-  static_assert(RPT >= 1 && MAXT % TEAMS == 0, "shape");
-  extern __shared__ __align__(128) float sm[];
-  __shared__ __align__(8) uint64_t full;
-  __shared__ DraftTile tiles[2];  // this tile and the next
+    draft_state_kernel(const DraftArgs p, const __grid_constant__ DraftMaps maps) {
+  constexpr int CT = st_cols(DV), TILES = DV / CT, NT = st_threads(MAXT);
+  constexpr int GROUPS = CT / 32, PARTS = st_parts(DK, DV, MAXT);
+  constexpr int KS = DK / PARTS / 16;       // steps of 16 rows of a warp
+  constexpr int RPT = 4 * KS;               // state rows of a thread (times 4 columns)
+  constexpr int TEAMS = NT / CT;            // threads per column behind the sums
+  constexpr int TPT = (MAXT + TEAMS - 1) / TEAMS;  // tokens of a team
+  constexpr int TG = MAXT / 4;              // groups of 4 tokens
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  float* sm = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                       ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int cq = tid % QL, row0 = (tid / QL) * RPT;
-  const int D = p.rec.depth, d_v = p.d_v, tiles_c = d_v / CT;
-  const unsigned total = (unsigned)p.n_seqs * (unsigned)(p.H_v * tiles_c);
+  const int cg = warp % GROUPS, part = warp / GROUPS;  // part >= PARTS: a warp without a share
+  const int fr = (lane & 3) * 2, fq = lane >> 2;       // first row and column quad of a fragment
+  const bool mine = part < PARTS;
+  const int row0 = part * (DK / PARTS) + fr;
+  const int D = p.rec.depth;
+  const unsigned per = (unsigned)(p.H_v * TILES), total = (unsigned)p.n_seqs * per;
   const uint8_t* ws = static_cast<const uint8_t*>(p.workspace);
   const int es = p.qkv_dtype == GDN_F32 ? 4 : 2;
 
-  float* st_s = sm;               // [DK][CT] state
+  // [GROUPS][DK][32] state; 16-byte groups of a row swizzled by the row (TMA's 128-byte mode), so
+  // that the 4 rows x 2 groups of a quarter-warp fall into different banks
+  float* st_s = sm;
   float* rk_s = st_s + DK * CT;   // [D][DK] accepted keys
-  float* uo_s = rk_s + D * DK;    // [D][CT] their u
-  // two sets of: keys and queries [2][T][DK], coefficients, v [T][CT] in its own type. Rows up to
-  // the next multiple of 4 tokens are read (what they give is dropped): at most 3 DK floats behind
-  // the last set's queries, all inside this block's memory.
-  float* late = uo_s + D * CT;
-  const int late_sz = late_floats(DK, CT, D, es);
-  float* red = late + 2 * late_sz;   // [warps][k, q][G][CT]
-  float* w_s = red + 2 * NW * G * CT;  // [MAXT][CT] right-hand sides of u
+  const int TR = 4 * token_groups(D);
+  float* uo_s = rk_s + D * DK;    // [TR][CT] their u
+  float2* fr_s = reinterpret_cast<float2*>(uo_s + TR * CT);  // keys and queries, see frag_bytes
+  // two sets of: v [TR][CT] in its own type, coefficients
+  float* late = uo_s + TR * CT + frag_bytes(DK, token_groups(D)) / 4;
+  const int late_sz = late_floats(CT, D, es);
+  float* red = late + 2 * late_sz;                // [parts][k, q][TR][CT]
+  uint64_t* full = reinterpret_cast<uint64_t*>(red + PARTS * 2 * TR * CT);
+  // tile number `it` of the block at [it & 3]: a slow warp may still read the one before when the
+  // next one is written
+  DraftTile* tiles = reinterpret_cast<DraftTile*>(full + 2);
 
-  // Loads of a tile, by warp 0: the state (unless the first tile has asked for it already) and
-  // the rest of what its sequence needs, all counted on `full`.
+  // Loads of a tile, all counted on `full`, by one thread of each of the first 4 warps (so that no
+  // warp is far behind the others at the next barrier). The keys and queries (load_frags) wait
+  // until the sums of the tile before are done; their bytes are expected here.
   auto load_tile = [&](const DraftTile& w, int set, bool with_state) {
-    const int T = w.hd.len, acc = w.hd.acc;
-    float* qk = late + set * late_sz;
-    float* cf = qk + 2 * D * DK;
-    uint8_t* vs = reinterpret_cast<uint8_t*>(cf + coef_size(D));
-    const int cbytes = coef_size(T) * 4;
-    if (lane == 0) {
-      umma::mbar_arrive_expect_tx(&full, (uint32_t)((with_state ? DK * CT * 4 : 0) +
-                                                    acc * (DK + CT) * 4 + 2 * T * DK * 4 + cbytes +
-                                                    T * CT * es));
+    uint8_t* vs = reinterpret_cast<uint8_t*>(late + set * late_sz);
+    if (warp == 0) {
+      umma::mbar_arrive_expect_tx(full, with_state ? DK * CT * 4 : 0);
+      // a zero state comes from behind the pool, where the copy fills in zeros
+      if (with_state)
+        umma::tma_load_4d(st_s, &maps.state, 0, 0, w.ct * GROUPS,
+                          w.hd.rst ? p.n_slots * p.H_v : w.hd.slot * p.H_v + w.h, full);
+    } else if (warp == 1) {
+      const int cbytes = coef_size(w.hd.len) * 4;
+      umma::mbar_arrive_expect_tx(full, cbytes + frag_bytes(DK, token_groups(w.hd.len)));
+      umma::bulk_g2s(vs + TR * CT * es, reinterpret_cast<const float*>(ws + p.ws_coef) +
+                                            ((int64_t)w.n * p.H_v + w.h) * DR_COEF, cbytes, full);
+    } else if (warp == 2) {
+      const int ga = token_groups(w.hd.acc);
+      umma::mbar_arrive_expect_tx(full, w.hd.acc * DK * 4 + ga * 16 * CT);
+      if (ga > 0) {
+        const int hk = khead_of(w.h, p.H_k, p.H_v, p.layout);
+        umma::bulk_g2s(rk_s, reinterpret_cast<const float*>(ws + p.ws_rk) +
+                                 ((int64_t)w.n * p.H_k + hk) * D * DK, w.hd.acc * DK * 4, full);
+      }
+      for (int g = 0; g < ga; ++g)
+        umma::tma_load_3d(uo_s + g * 4 * CT, &maps.u, w.ct * CT, g * 4, w.hd.slot * p.H_v + w.h,
+                          full);
+    } else if (warp == 3) {
+      const int gt = token_groups(w.hd.len);
+      umma::mbar_arrive_expect_tx(full, gt * 4 * CT * es);
+      for (int g = 0; g < gt; ++g)
+        umma::tma_load_2d(vs + g * 4 * CT * es, &maps.v, w.h * DV + w.ct * CT, w.hd.c0 + g * 4,
+                          full);
     }
-    __syncwarp();
-    const int hk = khead_of(w.h, p.H_k, p.H_v, p.layout);
-    const int64_t nk = (int64_t)w.n * p.H_k + hk;
-    if (lane == 0 && with_state)
-      umma::tma_load_3d(st_s, &tm_state, w.ct * CT, 0, w.hd.slot * p.H_v + w.h, &full);
-    if (lane == 1 && acc > 0)
-      umma::bulk_g2s(rk_s, reinterpret_cast<const float*>(ws + p.ws_rk) + nk * D * DK, acc * DK * 4,
-                     &full);
-    if (lane == 2 && T > 0)
-      umma::bulk_g2s(qk, reinterpret_cast<const float*>(ws + p.ws_qk) + nk * 2 * D * DK,
-                     2 * T * DK * 4, &full);
-    if (lane == 3)
-      umma::bulk_g2s(cf, reinterpret_cast<const float*>(ws + p.ws_coef) +
-                             ((int64_t)w.n * p.H_v + w.h) * DR_COEF, cbytes, &full);
-    if (lane < acc)
-      umma::bulk_g2s(uo_s + lane * CT,
-                     p.rec.u + (((int64_t)w.hd.slot * p.H_v + w.h) * D + lane) * d_v + w.ct * CT,
-                     CT * 4, &full);
-    if (lane >= 16 && lane - 16 < T)
-      umma::bulk_g2s(vs + (lane - 16) * CT * es,
-                     static_cast<const uint8_t*>(p.v) +
-                         (((int64_t)(w.hd.c0 + lane - 16) * p.H_v + w.h) * d_v + w.ct * CT) * es,
-                     CT * es, &full);
+  };
+  auto load_frags = [&](const DraftTile& w) {
+    if (w.hd.len > 0) {
+      const int hk = khead_of(w.h, p.H_k, p.H_v, p.layout);
+      umma::bulk_g2s(fr_s, ws + p.ws_qk + ((int64_t)w.n * p.H_k + hk) *
+                                              frag_bytes(DK, token_groups(D)),
+                     frag_bytes(DK, token_groups(w.hd.len)), full);
+    }
   };
 
   // ---- the first tile's state, before the first kernel's decision on its sequence is known (the
   // state was written before that kernel started)
-  unsigned t = blockIdx.x;
-  if (tid == 0) {
-    umma::mbar_init(&full, 1);
-    umma::fence_mbar_init();
-  }
-  if (warp == 0) {
-    __syncwarp();
-    DraftTile w = tile_at(p, t, tiles_c);
-    const int slot = p.slot_ids[w.n];
-    const bool rst = p.reset != nullptr && p.reset[w.n] != 0;
-    const bool idle = cu_at(p.cu_seqlens, w.n + 1) == cu_at(p.cu_seqlens, w.n) &&
-                      (!p.accepted || p.accepted[w.n] == 0);
-    const bool early = slot >= 0 && slot < p.n_slots && !rst && !idle;
-    if (early && lane == 0) {
-      umma::mbar_expect_tx(&full, DK * CT * 4);
-      umma::tma_load_3d(st_s, &tm_state, w.ct * CT, 0, slot * p.H_v + w.h, &full);
+  // Word `lane` of tile t (warp 0, lanes 0..11); zeros, nothing to do, for t >= total.
+  auto tile_word = [&](unsigned t) {
+    const unsigned n = t / per, rem = t - n * per;
+    if (t >= total || lane >= 12) return 0;
+    if (lane < 8) return reinterpret_cast<const int*>(ws + p.ws_hdr)[8 * (int64_t)n + lane];
+    return lane == 8 ? (int)n : lane == 9 ? (int)(rem / TILES) : lane == 10 ? (int)(rem % TILES) : 0;
+  };
+  // From the third on, tiles are taken in order by whichever block is free (drafts differ in
+  // length). Warp 0 is two tiles ahead: `t1` is the number of the next tile, `ahead` a word of it, `t2` the number of the
+  // one after, each asked for a tile before it is used.
+  unsigned* next = reinterpret_cast<unsigned*>(const_cast<uint8_t*>(ws) + p.ws_next);
+  auto take = [&]() {
+    unsigned t = 0;
+    if (lane == 0) t = 2 * gridDim.x + atomicAdd(next, 1u);
+    return t;
+  };
+  unsigned t1 = total, t2 = total;
+  int ahead = 0;
+  bool early = false;
+  {
+    const unsigned n = blockIdx.x / per, rem = blockIdx.x - n * per;
+    const int slot = p.slot_ids[n];
+    const bool rst = p.reset != nullptr && p.reset[n] != 0;
+    const bool idle = cu_at(p.cu_seqlens, n + 1) == cu_at(p.cu_seqlens, n) &&
+                      (!p.accepted || p.accepted[n] == 0);
+    early = slot >= 0 && slot < p.n_slots && !rst && !idle;
+    if (warp == 0) {
+      if (umma::elect_one()) {
+        umma::mbar_init(full, 4);
+        umma::fence_mbar_init();
+        if (early) {
+          umma::mbar_expect_tx(full, DK * CT * 4);
+          umma::tma_load_4d(st_s, &maps.state, 0, 0, (int)(rem % TILES) * GROUPS,
+                            slot * p.H_v + (int)(rem / TILES), full);
+        }
+      }
+      __syncwarp();
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    // what the first kernel wrote is read by bulk copies too
-    asm volatile("fence.proxy.async.global;" ::: "memory");
-    w.hd = header_at(p, w.n);
-    w.loaded = early || tile_works(w.hd);
-    if (tile_works(w.hd)) load_tile(w, 0, !early && !w.hd.rst);
-    else if (early && lane == 0) umma::mbar_arrive(&full);
-    if (lane == 0) tiles[0] = w;
-  } else {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // what the first kernel wrote is read by asynchronous copies too
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+  if (warp == 0) {
+    const int word = tile_word(blockIdx.x);
+    t1 = blockIdx.x + gridDim.x;
+    t2 = take();
+    ahead = tile_word(t1);
+    if (lane < 12) reinterpret_cast<int*>(&tiles[0])[lane] = lane == 11 ? t1 < total : word;
   }
   __syncthreads();
+  if (warp < 4 && umma::elect_one()) {
+    if (tile_works(tiles[0].hd)) {
+      load_tile(tiles[0], 0, !early);
+      if (warp == 1) load_frags(tiles[0]);
+    } else if (early) {
+      umma::mbar_arrive(full);
+    }
+  }
 
   uint32_t phase = 0;
-  for (int it = 0;; ++it, t += gridDim.x) {
-    const bool more = t + gridDim.x < total;
-    if (more && warp == 0) {
-      DraftTile w = tile_at(p, t + gridDim.x, tiles_c);
-      w.hd = header_at(p, w.n);
-      w.loaded = tile_works(w.hd);
-      if (lane == 0) tiles[(it + 1) & 1] = w;
+  for (int it = 0;; ++it) {
+    if (warp == 0 && t1 < total) {
+      t1 = __shfl_sync(0xffffffffu, t2, 0);
+      t2 = take();
+      if (lane < 12)
+        reinterpret_cast<int*>(&tiles[(it + 1) & 3])[lane] = lane == 11 ? t1 < total : ahead;
+      ahead = tile_word(t1);
     }
-    const DraftTile& cur = tiles[it & 1];
+    const DraftTile& cur = tiles[it & 3];
     const int T = cur.hd.len, acc = cur.hd.acc;
-    const bool rst = cur.hd.rst != 0, works = tile_works(cur.hd);
-    float* qk_s = late + (it & 1) * late_sz;
-    const float* cf = qk_s + 2 * D * DK;
+    const bool rst = cur.hd.rst != 0, works = tile_works(cur.hd), more = cur.more != 0;
+    const uint8_t* vs = reinterpret_cast<const uint8_t*>(late + (it & 1) * late_sz);
     const int TT = token_pad(T);
-    const float* cL = cf;                   // [TT][TT]: Lt[j][i]
+    const float* cL = reinterpret_cast<const float*>(vs + TR * CT * es);  // [TT][TT]: Lt[j][i]
     const float* cP = cL + TT * TT;         // [TT][TT]: P[i][j]
     const float* cC = cP + TT * TT;
     const float* cB = cC + TT;
     const float* cW = cB + TT;              // commit weights, then that of the old state
+    // rows row0 + 16 (m / 4) + 8 (m / 2 % 2) + m % 2, columns 32 cg + 4 fq ..
     float4 s[RPT];
-    if (cur.loaded) {
-      if (!umma::mbar_wait(&full, phase, nullptr)) {
+    auto row_of = [](int m) { return 16 * (m / 4) + 8 * (m / 2 % 2) + m % 2; };
+    if (works || (it == 0 && early)) {
+      if (!umma::mbar_wait(full, phase, nullptr)) {
         // the copies never came: give them as long again before the block's memory goes away
-        umma::mbar_wait(&full, phase, nullptr);
+        umma::mbar_wait(full, phase, nullptr);
         set_status(p.status, GDN_ETIMEOUT);
         return;
       }
       phase ^= 1;
     }
     if (cur.hd.run && tid == 0 && cur.h == 0 && cur.ct == 0) p.rec.n[cur.hd.slot] = T;
-    if (works) {
+    if (works && mine) {
+      const float* from = st_s + (cg * DK + row0) * 32;
 #pragma unroll
       for (int m = 0; m < RPT; ++m)
-        s[m] = rst ? make_float4(0.f, 0.f, 0.f, 0.f)
-                   : *reinterpret_cast<const float4*>(st_s + (row0 + m) * CT + cq * 4);
+        s[m] = *reinterpret_cast<const float4*>(from + row_of(m) * 32 +
+                                                ((fq ^ fr ^ (row_of(m) & 1)) << 2));
       // ---- commit
       if (acc > 0) {
         const float2 w0 = make_float2(cW[DR_MAX], cW[DR_MAX]);
@@ -606,118 +656,125 @@ __global__ void __launch_bounds__(st_threads(MAXT), st_blocks(MAXT))
 #pragma unroll 1
         for (int j = 0; j < acc; ++j) {
           const float w = cW[j];
-          const float4 u = *reinterpret_cast<const float4*>(uo_s + j * CT + cq * 4);
+          const float4 u = *reinterpret_cast<const float4*>(uo_s + j * CT + cg * 32 + fq * 4);
           const float2 ua = make_float2(u.x * w, u.y * w), ub = make_float2(u.z * w, u.w * w);
-          float kv[RPT];
-          load_rows<RPT>(kv, rk_s + j * DK + row0);
 #pragma unroll
-          for (int m = 0; m < RPT; ++m) {
-            const float2 kk = make_float2(kv[m], kv[m]);
-            const float2 x = fma2(kk, ua, make_float2(s[m].x, s[m].y));
-            const float2 y = fma2(kk, ub, make_float2(s[m].z, s[m].w));
-            s[m] = make_float4(x.x, x.y, y.x, y.y);
+          for (int m = 0; m < RPT; m += 2) {
+            const float2 k2 = *reinterpret_cast<const float2*>(rk_s + j * DK + row0 + row_of(m));
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const float k1 = b ? k2.y : k2.x;
+              const float2 kk = make_float2(k1, k1);
+              const float2 x = fma2(kk, ua, make_float2(s[m + b].x, s[m + b].y));
+              const float2 y = fma2(kk, ub, make_float2(s[m + b].z, s[m + b].w));
+              s[m + b] = make_float4(x.x, x.y, y.x, y.y);
+            }
           }
         }
       }
     }
     __syncthreads();  // the state, the old record and the sums of the tile before have been read
-    if (more && warp == 0) {
-      const DraftTile& w = tiles[(it + 1) & 1];
-      if (w.loaded) load_tile(w, (it + 1) & 1, !w.hd.rst);
+    const bool sums = works && T > 0;
+    const bool fetch = more && warp < 4 && tile_works(tiles[(it + 1) & 3].hd);
+    if (fetch && umma::elect_one()) {
+      load_tile(tiles[(it + 1) & 3], (it + 1) & 1, true);
+      if (!sums && warp == 1) load_frags(tiles[(it + 1) & 3]);
     }
-    if (works && (acc > 0 || rst)) {
-      float* S = p.state + (((int64_t)cur.hd.slot * p.H_v + cur.h) * DK + row0) * d_v +
-                 cur.ct * CT + cq * 4;
+    if (works && mine && (acc > 0 || rst)) {
+      float* S = p.state + (((int64_t)cur.hd.slot * p.H_v + cur.h) * DK + row0) * DV +
+                 cur.ct * CT + cg * 32 + fq * 4;
 #pragma unroll
-      for (int m = 0; m < RPT; ++m) st4_stream(S + (int64_t)m * d_v, s[m]);
+      for (int m = 0; m < RPT; ++m) st4_stream(S + row_of(m) * DV, s[m]);
     }
-    if (works && T > 0) {
-      const int team = tid / CT, col = tid % CT;
-      constexpr int QN = MAXT > TEAMS ? MAXT / TEAMS : 1;
-      float qs[QN];  // q sums of tokens team, team + TEAMS, ..
+    if (sums) {
+      const int ng = token_groups(T);
+      if (mine) {
+        // ---- column sums S^T k_t and S^T q_t of the warp's rows on the matrix unit, columns as M,
+        // vectors as N. An operand's first 11 bits go in as they are, the next 11 as a second
+        // operand; of their four products the one of both rests, 2^-22 of the whole, is left out.
+        // The large products and the others are summed apart: the adder cuts off what lies below
+        // its running sum's 24 bits.
+        float hi[TG][2][4], lo[TG][2][4];
 #pragma unroll
-      for (int g = 0; g < MAXT / G; ++g) {
-        if (g * G < T) {
-          const int cnt = T - g * G < G ? T - g * G : G;
-          // ---- column sums S^T k_t and S^T q_t, NRW tokens at a time
-#pragma unroll 1
-          for (int kind = 0; kind < 2; ++kind)
-#pragma unroll 1
-            for (int tb = 0; tb < cnt; tb += NRW) {
-              const float* vr = qk_s + (kind * T + g * G + tb) * DK + row0;
-              float x[NRW][4];
+        for (int g = 0; g < TG; ++g)
 #pragma unroll
-              for (int v = 0; v < NRW; v += 2) {
+          for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) x[v][c] = x[v + 1][c] = 0.f;
-                constexpr int kStep = RPT < 4 ? RPT : 4;
+            for (int c = 0; c < 4; ++c) hi[g][mt][c] = lo[g][mt][c] = 0.f;
 #pragma unroll
-                for (int m = 0; m < RPT; m += kStep) {
-                  float k0[kStep], k1[kStep];
-                  load_rows<kStep>(k0, vr + v * DK + m);
-                  load_rows<kStep>(k1, vr + (v + 1) * DK + m);
+        for (int k = 0; k < 2 * KS; ++k) {
+          // rows 2 k and 2 k + 1 of the thread; operand rows fq and fq + 8 are columns 4 fq + 2 mt
+          // and 4 fq + 2 mt + 1
+          const float4 x = s[2 * k], y = s[2 * k + 1];
+          const float4 xr = make_float4(tf32_rest(x.x), tf32_rest(x.y), tf32_rest(x.z), tf32_rest(x.w));
+          const float4 yr = make_float4(tf32_rest(y.x), tf32_rest(y.y), tf32_rest(y.z), tf32_rest(y.w));
 #pragma unroll
-                  for (int i = 0; i < kStep; ++i) {
-                    fma_row(x[v], s[m + i], k0[i]);
-                    fma_row(x[v + 1], s[m + i], k1[i]);
-                  }
-                }
-              }
-              // the NRW row groups of a warp share a column quad: halve the tokens at each
-              // exchange, so that a lane ends with one of them
-              int mine = 0;
-#pragma unroll
-              for (int half = NRW / 2, step = 16; half > 0; half /= 2, step /= 2) {
-                const bool hi = lane & step;
-#pragma unroll
-                for (int v = 0; v < half; ++v)
-#pragma unroll
-                  for (int c = 0; c < 4; ++c) {
-                    const float keep = hi ? x[v + half][c] : x[v][c];
-                    const float send = hi ? x[v][c] : x[v + half][c];
-                    x[v][c] = keep + __shfl_xor_sync(0xffffffffu, send, step);
-                  }
-                mine += hi ? half : 0;
-              }
-              *reinterpret_cast<float4*>(red + ((warp * 2 + kind) * G + tb + mine) * CT + cq * 4) =
-                  make_float4(x[0][0], x[0][1], x[0][2], x[0][3]);
-            }
-          __syncthreads();
-          // ---- per column, a token per team: the right-hand side of u, the q sum
-          auto col_sum = [&](int kind, int r) {
-            float y = 0.f;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) y += red[((w * 2 + kind) * G + r) * CT + col];
-            return y;
-          };
-          const uint8_t* vs = reinterpret_cast<const uint8_t*>(cf + coef_size(D));
-#pragma unroll
-          for (int r0 = 0; r0 < G; r0 += TEAMS) {
-            const int r = r0 + team, i = g * G + r;
-            if (r < G && i < T) {
-              const int at = i * CT + col;
-              const float v = p.qkv_dtype == GDN_F32    ? reinterpret_cast<const float*>(vs)[at]
-                              : p.qkv_dtype == GDN_BF16 ? ld(reinterpret_cast<const __nv_bfloat16*>(vs) + at)
-                                                        : ld(reinterpret_cast<const __half*>(vs) + at);
-              w_s[at] = cB[i] * (v - cC[i] * col_sum(0, r));
+          for (int g = 0; g < TG; ++g) {
+            if (g < ng) {
+              const float2 b = fr_s[(g * (DK / 8) + part * 2 * KS + k) * 32 + lane];
+              const float2 br = make_float2(tf32_rest(b.x), tf32_rest(b.y));
+              mma_tf32(hi[g][0], x.x, x.y, y.x, y.y, b);
+              mma_tf32(hi[g][1], x.z, x.w, y.z, y.w, b);
+              mma_tf32(lo[g][0], xr.x, xr.y, yr.x, yr.y, b);
+              mma_tf32(lo[g][1], xr.z, xr.w, yr.z, yr.w, b);
+              mma_tf32(lo[g][0], x.x, x.y, y.x, y.y, br);
+              mma_tf32(lo[g][1], x.z, x.w, y.z, y.w, br);
             }
           }
+        }
+        // a lane holds vectors fr and fr + 1 of a group, 4 columns; quads swizzled by the vector
 #pragma unroll
-          for (int j = 0; j < QN; ++j) {  // the team's tokens j TEAMS + team that are in this group
-            const int i = j * TEAMS + team, r = i - g * G;
-            if (r >= 0 && r < G && i < T) qs[j] = col_sum(1, r);
+        for (int g = 0; g < TG; ++g) {
+          if (g < ng) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const int v = fr + b;
+              float* rd = red + ((part * 2 + (v >> 2)) * TR + g * 4 + (v & 3)) * CT + cg * 32;
+              *reinterpret_cast<float4*>(rd + ((fq ^ v) << 2)) =
+                  make_float4(hi[g][0][b] + lo[g][0][b], hi[g][0][b + 2] + lo[g][0][b + 2],
+                              hi[g][1][b] + lo[g][1][b], hi[g][1][b + 2] + lo[g][1][b + 2]);
+            }
           }
-          __syncthreads();  // the sums have been read; the right-hand sides are there
         }
       }
-      float u[MAXT];
+      __syncthreads();  // the sums are there; the keys and queries have been read
+      if (fetch && warp == 1 && umma::elect_one()) load_frags(tiles[(it + 1) & 3]);
+
+      // ---- per column, a token per team: the right-hand side of u, the q sum
+      const int team = tid / CT, col = tid % CT;
+      auto place = [&](int kind, int i) {
+        return (kind * TR + i) * CT + (col & ~31) +
+               ((((col >> 2) & 7) ^ (kind * 4 + (i & 3))) << 2) + (col & 3);
+      };
+      auto col_sum = [&](int at) {
+        float y = 0.f;
 #pragma unroll
-      for (int i = 0; i < MAXT; ++i) u[i] = i < T ? w_s[i * CT + col] : 0.f;
-      float* recu = p.rec.u + ((int64_t)cur.hd.slot * p.H_v + cur.h) * D * d_v + cur.ct * CT + col;
-      const int64_t tok = (int64_t)p.H_v * d_v;
-      const int64_t o0 = ((int64_t)cur.hd.c0 * p.H_v + cur.h) * d_v + cur.ct * CT + col;
+        for (int w = 0; w < PARTS; ++w) y += red[w * 2 * TR * CT + at];
+        return y;
+      };
+      float qs[TPT];  // of tokens team, team + TEAMS, ..
+#pragma unroll
+      for (int j = 0; j < TPT; ++j) {
+        const int i = j * TEAMS + team;
+        if (i < T) {
+          const int at = i * CT + col;
+          const float v = p.qkv_dtype == GDN_F32    ? reinterpret_cast<const float*>(vs)[at]
+                          : p.qkv_dtype == GDN_BF16 ? ld(reinterpret_cast<const __nv_bfloat16*>(vs) + at)
+                                                    : ld(reinterpret_cast<const __half*>(vs) + at);
+          const int k = place(0, i);  // read by this thread alone: the right-hand side takes its place
+          red[k] = cB[i] * (v - cC[i] * col_sum(k));
+          qs[j] = col_sum(place(1, i));
+        }
+      }
+      __syncthreads();  // the right-hand sides are there
+      float* recu = p.rec.u + ((int64_t)cur.hd.slot * p.H_v + cur.h) * D * DV + cur.ct * CT + col;
+      const int64_t tok = (int64_t)p.H_v * DV;
+      const int64_t o0 = ((int64_t)cur.hd.c0 * p.H_v + cur.h) * DV + cur.ct * CT + col;
       auto finish = [&](auto tt) {
         constexpr int N = decltype(tt)::value;
+        float u[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) u[i] = i < T ? red[place(0, i)] : 0.f;
         // the triangular solve; rows of the tables at and behind T are zero
 #pragma unroll
         for (int j = 0; j < N - 1; ++j)
@@ -737,7 +794,7 @@ __global__ void __launch_bounds__(st_threads(MAXT), st_blocks(MAXT))
 #pragma unroll
             for (int m = 1; m < TEAMS && r * TEAMS + m < N; ++m)
               ui = team == m ? u[r * TEAMS + m] : ui;
-            recu[(int64_t)i * d_v] = ui;
+            recu[i * DV] = ui;
             float o = cC[i] * qs[r];
 #pragma unroll
             for (int j4 = 0; 4 * j4 < N && 4 * j4 <= r * TEAMS + TEAMS - 1; ++j4) {
@@ -752,7 +809,7 @@ __global__ void __launch_bounds__(st_threads(MAXT), st_blocks(MAXT))
           }
         }
       };
-      if (TT == 4) finish(std::integral_constant<int, 4>{});
+      if (MAXT == 4 || TT == 4) finish(std::integral_constant<int, 4>{});
       else if (MAXT == 8 || TT == 8) finish(std::integral_constant<int, 8>{});
       else finish(std::integral_constant<int, MAXT>{});
     }
@@ -789,11 +846,13 @@ __global__ void __launch_bounds__(256) draft_gate_kernel(const DraftArgs p, cons
 
 int prep_smem(int d_k, int r, int depth) {
   const int td = token_pad(depth);
-  return (2 * td * (d_k + 4) + 4 * 2 * td * td + 3 * r * DR_MAX) * 4;
+  return (2 * td * (d_k + 8) + 4 * 2 * td * td + 3 * r * DR_MAX) * 4;
 }
-int state_smem(int d_k, int ct, int max_t, int depth, int es) {
-  return (d_k * ct + depth * (d_k + ct) + 2 * late_floats(d_k, ct, depth, es) +
-          2 * (st_threads(max_t) / 32) * ST_GROUP * ct + max_t * ct) * 4;
+int state_smem(int d_k, int d_v, int max_t, int depth, int es) {
+  const int rows = 4 * token_groups(depth), ct = st_cols(d_v);
+  return (d_k * ct + depth * d_k + rows * ct + 2 * late_floats(ct, depth, es) +
+          st_parts(d_k, d_v, max_t) * 2 * rows * ct) * 4 +
+         frag_bytes(d_k, token_groups(depth)) + 16 + 4 * (int)sizeof(DraftTile) + 1024;
 }
 
 template <int DK, typename TX, typename TS, bool FUSED>
@@ -835,39 +894,60 @@ cudaError_t launch_prep_k(const DraftArgs& a, cudaStream_t s) {
   return cudaErrorInvalidValue;
 }
 
-// The state pool as [heads of all slots][d_k][d_v] fp32, a box of d_k rows x ct columns.
-cudaError_t state_map(CUtensorMap* m, const DraftArgs& a, int ct) {
-  const TensorMapEncodeFn enc = tensor_map_encode();
-  if (!enc) return cudaErrorNotSupported;
-  const int64_t heads = (int64_t)a.n_slots * a.H_v;
-  if (heads > 0x7fffffff) return cudaErrorInvalidValue;
-  const cuuint64_t dims[3] = {(cuuint64_t)a.d_v, (cuuint64_t)a.d_k, (cuuint64_t)heads};
-  const cuuint64_t strides[2] = {(cuuint64_t)a.d_v * 4, (cuuint64_t)a.d_k * a.d_v * 4};
-  const cuuint32_t box[3] = {(cuuint32_t)ct, (cuuint32_t)a.d_k, 1}, estr[3] = {1, 1, 1};
-  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, a.state, dims, strides, box, estr,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+// A tensor map of `rank` dimensions, innermost first; strides of all but the first, in bytes.
+bool encode(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base,
+            const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box, bool swizzle) {
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return tensor_map_encode()(
+             m, type, rank, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE,
+             swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+cudaError_t draft_maps(DraftMaps* m, const DraftArgs& a, int ct) {
+  if (!tensor_map_encode()) return cudaErrorNotSupported;
+  const int64_t heads = (int64_t)a.n_slots * a.H_v, width = (int64_t)a.H_v * a.d_v;
+  if (heads > 0x7fffffff || width > 0x7fffffff || a.T_total > 0x7fffffff)
+    return cudaErrorInvalidValue;
+  const cuuint64_t row = (cuuint64_t)a.d_v * 4;
+  const cuuint64_t sd[4] = {32, (cuuint64_t)a.d_k, (cuuint64_t)a.d_v / 32, (cuuint64_t)heads};
+  const cuuint64_t ss[3] = {row, 128, row * a.d_k};
+  const cuuint32_t sb[4] = {32, (cuuint32_t)a.d_k, (cuuint32_t)ct / 32, 1};
+  const cuuint64_t ud[3] = {(cuuint64_t)a.d_v, (cuuint64_t)a.rec.depth, (cuuint64_t)heads};
+  const cuuint64_t us[2] = {row, row * a.rec.depth};
+  const cuuint32_t ub[3] = {(cuuint32_t)ct, 4, 1};
+  const CUtensorMapDataType vt = a.qkv_dtype == GDN_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                 : a.qkv_dtype == GDN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                           : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const cuuint64_t vd[2] = {(cuuint64_t)width, (cuuint64_t)(a.T_total > 0 ? a.T_total : 1)};
+  const cuuint64_t vs[1] = {(cuuint64_t)width * (a.qkv_dtype == GDN_F32 ? 4 : 2)};
+  const cuuint32_t vb[2] = {(cuuint32_t)ct, 4};
+  // no tokens: v may be null, and nothing is read through its map
+  const bool ok =
+      encode(&m->state, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.state, sd, ss, sb, true) &&
+      encode(&m->u, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, a.rec.u, ud, us, ub, false) &&
+      encode(&m->v, vt, 2, a.T_total > 0 ? a.v : a.rec.u, vd, vs, vb, false);
+  return ok ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int DK, int CT, int MAXT>
+template <int DK, int DV, int MAXT>
 cudaError_t launch_state(const DraftArgs& a, cudaStream_t s) {
-  auto kern = draft_state_kernel<DK, CT, MAXT>;
-  alignas(64) CUtensorMap tm;
-  cudaError_t e = state_map(&tm, a, CT);
+  auto kern = draft_state_kernel<DK, DV, MAXT>;
+  alignas(64) DraftMaps maps;
+  cudaError_t e = draft_maps(&maps, a, st_cols(DV));
   if (e != cudaSuccess) return e;
   const int es = a.qkv_dtype == GDN_F32 ? 4 : 2;
-  const int bytes = state_smem(DK, CT, MAXT, a.rec.depth, es);
+  const int bytes = state_smem(DK, DV, MAXT, a.rec.depth, es);
   static std::atomic<int> smem_set[64];
   // for the largest depth, so that the limit is set once
-  e = allow_smem(kern, state_smem(DK, CT, MAXT, MAXT, 4), smem_set);
+  e = allow_smem(kern, state_smem(DK, DV, MAXT, MAXT, 4), smem_set);
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
   if (sms == 0) return cudaErrorInvalidDevice;
   // as many blocks as fit at once: 228 KB of shared memory per SM, 1 KB of it per block reserved
-  int per_sm = 228 * 1024 / (bytes + 1024 + 128);
+  int per_sm = 228 * 1024 / (bytes + 1024);
   if (per_sm > st_blocks(MAXT)) per_sm = st_blocks(MAXT);
-  const int64_t total = (int64_t)a.n_seqs * a.H_v * (a.d_v / CT);
+  const int64_t total = (int64_t)a.n_seqs * a.H_v * (DV / st_cols(DV));
   if (total > 0x7fffffff) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -879,12 +959,13 @@ cudaError_t launch_state(const DraftArgs& a, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a, tm);
+  return cudaLaunchKernelEx(&cfg, kern, a, maps);
 }
 
-template <int DK, int CT>
+template <int DK, int DV>
 cudaError_t launch_state_t(const DraftArgs& a, cudaStream_t s) {
-  return a.rec.depth <= 8 ? launch_state<DK, CT, 8>(a, s) : launch_state<DK, CT, DR_MAX>(a, s);
+  if (a.rec.depth <= 4) return launch_state<DK, DV, 4>(a, s);
+  return a.rec.depth <= 8 ? launch_state<DK, DV, 8>(a, s) : launch_state<DK, DV, DR_MAX>(a, s);
 }
 
 template <int VPL, typename TZ, typename TO>
@@ -920,7 +1001,12 @@ cudaError_t launch_both(const DraftArgs& a0, cudaStream_t s) {
     a.v = static_cast<uint8_t*>(a.workspace) + a.ws_v;
     a.qkv_dtype = GDN_F32;
   }
-  return a.d_v % 64 == 0 ? launch_state_t<DK, 64>(a, s) : launch_state_t<DK, 32>(a, s);
+  switch (a.d_v) {
+    case 32: return launch_state_t<DK, 32>(a, s);
+    case 64: return launch_state_t<DK, 64>(a, s);
+    case 128: return launch_state_t<DK, 128>(a, s);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -932,8 +1018,7 @@ size_t draft_workspace(int H_k, int H_v, int d_k, int d_v, int64_t T_total, int 
 cudaError_t launch_draft(const DraftArgs& a0, const GateArgs* gate, cudaStream_t s) {
   DraftArgs a = a0;
   const DraftWs w = draft_ws(a.H_k, a.H_v, a.d_k, a.d_v, a.T_total, a.n_seqs, a.rec.depth);
-  a.pf_blocks = (int)(kStateAhead / ((int64_t)(a.H_v / a.H_k) * a.d_k * a.d_v * 4));
-  a.ws_hdr = w.hdr; a.ws_qk = w.qk; a.ws_rk = w.rk; a.ws_coef = w.coef; a.ws_v = w.v;
+  a.ws_next = w.next; a.ws_hdr = w.hdr; a.ws_qk = w.qk; a.ws_rk = w.rk; a.ws_coef = w.coef; a.ws_v = w.v;
   GateArgs g{};
   if (gate) {
     g = *gate;

@@ -101,8 +101,7 @@ struct DraftArgs {
   int layout;
   int32_t* status;
   // set by the launcher: byte offsets of the workspace's parts
-  size_t ws_hdr, ws_qk, ws_rk, ws_coef, ws_v;
-  int pf_blocks;  // blocks of the first kernel that ask L2 for their states
+  size_t ws_next, ws_hdr, ws_qk, ws_rk, ws_coef, ws_v;
 };
 
 // out[m][n] = act(sum_k x[m][k] w[n][k] + bias[n]) + residual[m][n]; strides in elements.
