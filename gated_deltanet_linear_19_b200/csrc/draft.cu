@@ -471,7 +471,6 @@ __global__ void __launch_bounds__(st_threads(MAXT), st_blocks(MAXT))
   constexpr int RPT = 4 * KS;               // state rows of a thread (times 4 columns)
   constexpr int TEAMS = NT / CT;            // threads per column behind the sums
   constexpr int TPT = (MAXT + TEAMS - 1) / TEAMS;  // tokens of a team
-  constexpr int TG = MAXT / 4;              // groups of 4 tokens
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   float* sm = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                        ~static_cast<uintptr_t>(1023));
@@ -694,46 +693,38 @@ __global__ void __launch_bounds__(st_threads(MAXT), st_blocks(MAXT))
         // operand; of their four products the one of both rests, 2^-22 of the whole, is left out.
         // The large products and the others are summed apart: the adder cuts off what lies below
         // its running sum's 24 bits.
-        float hi[TG][2][4], lo[TG][2][4];
-#pragma unroll
-        for (int g = 0; g < TG; ++g)
+        // One group of 4 tokens after another in a loop: unrolled over the groups, the code no longer
+        // fits the instruction cache (one token per sequence, depth 16: 70.5 us).
+#pragma unroll 1
+        for (int g = 0; g < ng; ++g) {
+          float hi[2][4], lo[2][4];
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) hi[g][mt][c] = lo[g][mt][c] = 0.f;
+            for (int c = 0; c < 4; ++c) hi[mt][c] = lo[mt][c] = 0.f;
+          const float2* f = fr_s + (g * (DK / 8) + part * 2 * KS) * 32 + lane;
 #pragma unroll
-        for (int k = 0; k < 2 * KS; ++k) {
-          // rows 2 k and 2 k + 1 of the thread; operand rows fq and fq + 8 are columns 4 fq + 2 mt
-          // and 4 fq + 2 mt + 1
-          const float4 x = s[2 * k], y = s[2 * k + 1];
-          const float4 xr = make_float4(tf32_rest(x.x), tf32_rest(x.y), tf32_rest(x.z), tf32_rest(x.w));
-          const float4 yr = make_float4(tf32_rest(y.x), tf32_rest(y.y), tf32_rest(y.z), tf32_rest(y.w));
-#pragma unroll
-          for (int g = 0; g < TG; ++g) {
-            if (g < ng) {
-              const float2 b = fr_s[(g * (DK / 8) + part * 2 * KS + k) * 32 + lane];
-              const float2 br = make_float2(tf32_rest(b.x), tf32_rest(b.y));
-              mma_tf32(hi[g][0], x.x, x.y, y.x, y.y, b);
-              mma_tf32(hi[g][1], x.z, x.w, y.z, y.w, b);
-              mma_tf32(lo[g][0], xr.x, xr.y, yr.x, yr.y, b);
-              mma_tf32(lo[g][1], xr.z, xr.w, yr.z, yr.w, b);
-              mma_tf32(lo[g][0], x.x, x.y, y.x, y.y, br);
-              mma_tf32(lo[g][1], x.z, x.w, y.z, y.w, br);
-            }
+          for (int k = 0; k < 2 * KS; ++k) {
+            // rows 2 k and 2 k + 1 of the thread; operand rows fq and fq + 8 are columns 4 fq + 2 mt
+            // and 4 fq + 2 mt + 1
+            const float4 x = s[2 * k], y = s[2 * k + 1];
+            const float2 b = f[k * 32];
+            const float2 br = make_float2(tf32_rest(b.x), tf32_rest(b.y));
+            mma_tf32(hi[0], x.x, x.y, y.x, y.y, b);
+            mma_tf32(hi[1], x.z, x.w, y.z, y.w, b);
+            mma_tf32(lo[0], x.x, x.y, y.x, y.y, br);
+            mma_tf32(lo[1], x.z, x.w, y.z, y.w, br);
+            mma_tf32(lo[0], tf32_rest(x.x), tf32_rest(x.y), tf32_rest(y.x), tf32_rest(y.y), b);
+            mma_tf32(lo[1], tf32_rest(x.z), tf32_rest(x.w), tf32_rest(y.z), tf32_rest(y.w), b);
           }
-        }
-        // a lane holds vectors fr and fr + 1 of a group, 4 columns; quads swizzled by the vector
+          // a lane holds vectors fr and fr + 1 of the group, 4 columns; quads swizzled by the vector
 #pragma unroll
-        for (int g = 0; g < TG; ++g) {
-          if (g < ng) {
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              const int v = fr + b;
-              float* rd = red + ((part * 2 + (v >> 2)) * TR + g * 4 + (v & 3)) * CT + cg * 32;
-              *reinterpret_cast<float4*>(rd + ((fq ^ v) << 2)) =
-                  make_float4(hi[g][0][b] + lo[g][0][b], hi[g][0][b + 2] + lo[g][0][b + 2],
-                              hi[g][1][b] + lo[g][1][b], hi[g][1][b + 2] + lo[g][1][b + 2]);
-            }
+          for (int b = 0; b < 2; ++b) {
+            const int v = fr + b;
+            float* rd = red + ((part * 2 + (v >> 2)) * TR + g * 4 + (v & 3)) * CT + cg * 32;
+            *reinterpret_cast<float4*>(rd + ((fq ^ v) << 2)) =
+                make_float4(hi[0][b] + lo[0][b], hi[0][b + 2] + lo[0][b + 2],
+                            hi[1][b] + lo[1][b], hi[1][b + 2] + lo[1][b + 2]);
           }
         }
       }
