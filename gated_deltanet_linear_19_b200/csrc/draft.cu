@@ -216,23 +216,41 @@ __global__ void __launch_bounds__(DR_THREADS, FUSED ? 4 : 7) draft_prep_kernel(c
       if (tid + x * DR_THREADS < acc * LPH)
         reinterpret_cast<float4*>(rk)[tid + x * DR_THREADS] = old[x];
   };
-  // Gates of the key head's value heads, old and new decays.
-  auto gates = [&]() {
-    for (int i = tid; i < r * DR_MAX; i += DR_THREADS) {
-      const int jv = i / DR_MAX, t = i % DR_MAX;
-      const int h = (p.layout & GDN_GQA_TILED) ? hk + jv * p.H_k : hk * r + jv;
-      if (t < acc) go[i] = p.rec.e[((int64_t)slot * p.H_v + h) * D + t];
-      if (t < T) {
-        if constexpr (FUSED) {
-          const float z = gate_alpha(p.fa, c0 + t, h, p.H_k, p.H_v, p.layout) + p.dt_bias[h];
-          ge[i] = expf(-expf(p.A_log[h]) * softplusf_(z));
-          gb[i] = sigmoidf_(gate_beta_logit(p.fa, p.fb, c0 + t, h, p.H_k, p.H_v, p.layout));
-        } else {
-          ge[i] = expf(p.g[(c0 + t) * p.H_v + h]);
-          gb[i] = p.beta[(c0 + t) * p.H_v + h];
-        }
+  // Gates of the key head's value heads, old and new decays: a token of a head per thread, the last
+  // warp first (it has the least else to do); asked for here, used behind the other loads.
+  struct Gate {
+    float a, b, rate, bias, old;
+  };
+  auto gate_load = [&](int i) {
+    Gate g{};
+    const int jv = i / DR_MAX, t = i % DR_MAX;
+    if (jv >= r) return g;
+    const int h = (p.layout & GDN_GQA_TILED) ? hk + jv * p.H_k : hk * r + jv;
+    if (t < acc) g.old = p.rec.e[((int64_t)slot * p.H_v + h) * D + t];
+    if (t < T) {
+      if constexpr (FUSED) {
+        g.a = gate_alpha(p.fa, c0 + t, h, p.H_k, p.H_v, p.layout);
+        g.b = gate_beta_logit(p.fa, p.fb, c0 + t, h, p.H_k, p.H_v, p.layout);
+        g.rate = p.A_log[h];
+        g.bias = p.dt_bias[h];
+      } else {
+        g.a = p.g[(c0 + t) * p.H_v + h];
+        g.b = p.beta[(c0 + t) * p.H_v + h];
       }
     }
+    return g;
+  };
+  auto gate_put = [&](int i, const Gate& g) {
+    if (i >= r * DR_MAX) return;
+    go[i] = g.old;
+    ge[i] = FUSED ? expf(-expf(g.rate) * softplusf_(g.a + g.bias)) : expf(g.a);
+    gb[i] = FUSED ? sigmoidf_(g.b) : g.b;
+  };
+  const int gate0 = DR_THREADS - 1 - tid;
+  const Gate gate = gate_load(gate0);
+  auto gates = [&]() {
+    gate_put(gate0, gate);
+    for (int i = gate0 + DR_THREADS; i < r * DR_MAX; i += DR_THREADS) gate_put(i, gate_load(i));
   };
 
   // ---- q and k of the tokens into shared memory and v to the workspace, from raw x
@@ -243,7 +261,7 @@ __global__ void __launch_bounds__(DR_THREADS, FUSED ? 4 : 7) draft_prep_kernel(c
     TS* recx = R > 0 ? static_cast<TS*>(p.rec.x) + (int64_t)slot * D * conv_dim : nullptr;
     const TX* xg = static_cast<const TX*>(p.x);
     float* vg = reinterpret_cast<float*>(ws + p.ws_v);
-    const int vq = p.d_v / 4;
+    const int vq = p.d_v / 4, vq_log = __ffs(vq) - 1;  // d_v is 32, 64 or 128
     // warp 0: q, warp 1: k, warps 2 and 3: the v quads of the r value heads
     const int n_item = warp < 2 ? 1 : (r * vq + 63 - (tid - 64)) / 64;
     bool settled = false;
@@ -256,7 +274,7 @@ __global__ void __launch_bounds__(DR_THREADS, FUSED ? 4 : 7) draft_prep_kernel(c
         if (active) ch = (int64_t)warp * p.H_k * DK + (int64_t)hk * DK + lane * 4;
       } else if (active) {
         const int item = tid - 64 + it * 64;
-        jv = item / vq; qd = item % vq;
+        jv = item >> vq_log; qd = item & (vq - 1);
         const int h = (p.layout & GDN_GQA_TILED) ? hk + jv * p.H_k : hk * r + jv;
         ch = 2LL * p.H_k * DK + (int64_t)h * p.d_v + qd * 4;
       }
@@ -296,9 +314,9 @@ __global__ void __launch_bounds__(DR_THREADS, FUSED ? 4 : 7) draft_prep_kernel(c
                                   : make_float4(0.f, 0.f, 0.f, 0.f);
       if (!settled) {
         settled = true;
-        gates();
         keep_keys();
         if (!settle()) return;
+        gates();
       }
       if (active && R > 0 && (acc > 0 || rst)) {
 #pragma unroll
@@ -310,70 +328,85 @@ __global__ void __launch_bounds__(DR_THREADS, FUSED ? 4 : 7) draft_prep_kernel(c
         }
       }
       for (int tb = 0; tb < T; tb += 4) {
+        float y[4][4], ss[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int t = tb + u;
-          if (t >= T) break;
-          const float xs[4] = {xr[u].x, xr[u].y, xr[u].z, xr[u].w};
-          if (active && R > 0) st4(recx + (int64_t)t * conv_dim + ch, xr[u]);
-          float y[4], ss = 0.f;
+          ss[u] = 0.f;
+          if (t < T) {
+            const float xs[4] = {xr[u].x, xr[u].y, xr[u].z, xr[u].w};
+            if (active && R > 0) st4(recx + (int64_t)t * conv_dim + ch, xr[u]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (p.d_conv > 0) {
-              float a = wa[j][0] * win[0][j];
-              a = fmaf(wa[j][1], win[1][j], a);
-              a = fmaf(wa[j][2], win[2][j], a);
-              a = fmaf(wa[j][3], xs[j], a);
-              y[j] = a * sigmoidf_(a);
-            } else {
-              y[j] = xs[j];
+            for (int j = 0; j < 4; ++j) {
+              y[u][j] = xs[j];
+              if (p.d_conv > 0) {
+                float a = wa[j][0] * win[0][j];
+                a = fmaf(wa[j][1], win[1][j], a);
+                a = fmaf(wa[j][2], win[2][j], a);
+                a = fmaf(wa[j][3], xs[j], a);
+                // the division within 2 steps of fp32; a / inf = 0 far below zero
+                y[u][j] = __fdividef(a, 1.0f + expf(-a));
+              }
+              ss[u] = fmaf(y[u][j], y[u][j], ss[u]);
+              win[0][j] = win[1][j];
+              win[1][j] = win[2][j];
+              win[2][j] = xs[j];
             }
-            ss = fmaf(y[j], y[j], ss);
-            win[0][j] = win[1][j];
-            win[1][j] = win[2][j];
-            win[2][j] = xs[j];
+            // the next four tokens' inputs are asked for as these are used
+            if (active && t + 4 < T) xr[u] = ld4(xg + (c0 + t + 4) * conv_dim + ch);
           }
-          // the next four tokens' inputs are asked for as these are used
-          if (active && t + 4 < T) xr[u] = ld4(xg + (c0 + t + 4) * conv_dim + ch);
-          if (warp < 2) {
-            const float mul = (warp == 0 ? p.q_scale : 1.0f) / sqrtf(warp_sum(ss) + p.eps);
-            if (active)
-              *reinterpret_cast<float4*>(vec + ((warp == 0 ? T4 : 0) + t) * LDV + lane * 4) =
-                  make_float4(y[0] * mul, y[1] * mul, y[2] * mul, y[3] * mul);
-          } else if (active) {
-            const int h = (p.layout & GDN_GQA_TILED) ? hk + jv * p.H_k : hk * r + jv;
-            *reinterpret_cast<float4*>(vg + ((c0 + t) * p.H_v + h) * p.d_v + qd * 4) =
-                make_float4(y[0], y[1], y[2], y[3]);
+        }
+        if (warp < 2) {
+          // the four tokens' sums side by side
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) ss[u] += __shfl_xor_sync(0xffffffffu, ss[u], o);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float mul = (warp == 0 ? p.q_scale : 1.0f) / sqrtf(ss[u] + p.eps);
+            if (active && tb + u < T)
+              *reinterpret_cast<float4*>(vec + ((warp == 0 ? T4 : 0) + tb + u) * LDV + lane * 4) =
+                  make_float4(y[u][0] * mul, y[u][1] * mul, y[u][2] * mul, y[u][3] * mul);
           }
+        } else if (active) {
+          const int h = (p.layout & GDN_GQA_TILED) ? hk + jv * p.H_k : hk * r + jv;
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (tb + u < T)
+              *reinterpret_cast<float4*>(vg + ((c0 + tb + u) * p.H_v + h) * p.d_v + qd * 4) =
+                  make_float4(y[u][0], y[u][1], y[u][2], y[u][3]);
         }
       }
     }
     __syncthreads();
   } else {
+    const int half = T * LPH;  // items of the keys, then as many of the queries
     auto from = [&](int i) {
-      const int w = i / (T * LPH), t = i / LPH - w * T, d = (i % LPH) * 4;
-      return ld4(static_cast<const TX*>(w ? p.q : p.k) + ((c0 + t) * p.H_k + hk) * DK + d);
+      const bool is_q = i >= half;
+      const int j = is_q ? i - half : i, t = j / LPH, d = (j % LPH) * 4;
+      return ld4(static_cast<const TX*>(is_q ? p.q : p.k) + ((c0 + t) * p.H_k + hk) * DK + d);
     };
     auto put = [&](int i, float4 v) {
-      const int w = i / (T * LPH), t = i / LPH - w * T, d = (i % LPH) * 4;
-      *reinterpret_cast<float4*>(vec + (w * T4 + t) * LDV + d) = v;
+      const int j = i >= half ? i - half : i, t = j / LPH + (i >= half ? T4 : 0);
+      *reinterpret_cast<float4*>(vec + t * LDV + (j % LPH) * 4) = v;
     };
     float4 in[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x)
-      if (tid + x * DR_THREADS < 2 * T * LPH) in[x] = from(tid + x * DR_THREADS);
-    gates();
+      if (tid + x * DR_THREADS < 2 * half) in[x] = from(tid + x * DR_THREADS);
     keep_keys();
 #pragma unroll
     for (int x = 0; x < 2; ++x)
-      if (tid + x * DR_THREADS < 2 * T * LPH) put(tid + x * DR_THREADS, in[x]);
+      if (tid + x * DR_THREADS < 2 * half) put(tid + x * DR_THREADS, in[x]);
 #pragma unroll 4
-    for (int i = tid + 2 * DR_THREADS; i < 2 * T * LPH; i += DR_THREADS) put(i, from(i));
+    for (int i = tid + 2 * DR_THREADS; i < 2 * half; i += DR_THREADS) put(i, from(i));
+    gates();
     if (!settle()) return;
   }
 
-  // ---- the new record's decays and keys, and q and k for the state kernel (rows behind the last token of a
-  // group hold anything: what they give is dropped)
+  // ---- the new record's decays and keys, and q and k for the state kernel (rows behind the last
+  // token of a group hold anything: what they give is dropped)
   for (int i = tid; i < r * DR_MAX; i += DR_THREADS) {
     const int jv = i / DR_MAX, t = i % DR_MAX;
     const int h = (p.layout & GDN_GQA_TILED) ? hk + jv * p.H_k : hk * r + jv;
@@ -396,8 +429,9 @@ __global__ void __launch_bounds__(DR_THREADS, FUSED ? 4 : 7) draft_prep_kernel(c
   else token_dots<4, DK>(vec, part);
   __syncthreads();
   float* coef = reinterpret_cast<float*>(ws + p.ws_coef);
-  for (int i = tid; i < r * T4 * T4; i += DR_THREADS) {
-    const int jv = i / (T4 * T4), row = (i / T4) % T4, col = i % T4;
+  const int lt = T4 == 4 ? 2 : T4 == 8 ? 3 : 4;
+  for (int i = tid; i < r << (2 * lt); i += DR_THREADS) {
+    const int jv = i >> (2 * lt), row = (i >> lt) & (T4 - 1), col = i & (T4 - 1);
     const int h = (p.layout & GDN_GQA_TILED) ? hk + jv * p.H_k : hk * r + jv;
     float* cL = coef + ((int64_t)n * p.H_v + h) * DR_COEF;
     float* cP = cL + T4 * T4;
@@ -421,8 +455,9 @@ __global__ void __launch_bounds__(DR_THREADS, FUSED ? 4 : 7) draft_prep_kernel(c
       cC[T4 + col] = gb[jv * DR_MAX + col];
     }
   }
-  for (int i = tid; i < r * acc; i += DR_THREADS) {
-    const int jv = i / acc, j = i - jv * acc;
+  for (int i = tid; i < r * DR_MAX; i += DR_THREADS) {
+    const int jv = i / DR_MAX, j = i % DR_MAX;
+    if (j >= acc) continue;
     const int h = (p.layout & GDN_GQA_TILED) ? hk + jv * p.H_k : hk * r + jv;
     float* cW = coef + ((int64_t)n * p.H_v + h) * DR_COEF + 2 * T4 * T4 + 2 * T4;
     float w = 1.f;
@@ -449,24 +484,21 @@ struct DraftMaps {
   CUtensorMap state, v, u;
 };
 
-// Shape of the state kernel for records of up to max_t tokens: 16 warps on an SM either way, in
-// blocks as large as what their inputs need of shared memory asks for (64 sequences x 0..16
-// tokens: 107 us with two blocks of 4 warps on an SM).
-__host__ __device__ constexpr int st_threads(int max_t) { return 128; }
+// Blocks of the state kernel on an SM, at most, for records of up to max_t tokens: what their
+// inputs leave room for in shared memory. (Blocks of 8 warps, half the rows each, were slower at
+// every depth: 64 sequences x 1 token, depth 16, 88.6 us against 70.5.)
 __host__ __device__ constexpr int st_blocks(int max_t) { return max_t <= 4 ? 4 : max_t <= 8 ? 3 : 2; }
 // Columns of a tile; the warps of a block: ct / 32 side by side, st_parts below each other.
 __host__ __device__ constexpr int st_cols(int d_v) { return d_v < 64 ? d_v : 64; }
-__host__ __device__ constexpr int st_parts(int d_k, int d_v, int max_t) {
-  return st_threads(max_t) / 32 / (st_cols(d_v) / 32) < d_k / 16
-             ? st_threads(max_t) / 32 / (st_cols(d_v) / 32)
-             : d_k / 16;
+__host__ __device__ constexpr int st_parts(int d_k, int d_v) {
+  return 4 / (st_cols(d_v) / 32) < d_k / 16 ? 4 / (st_cols(d_v) / 32) : d_k / 16;
 }
 
 template <int DK, int DV, int MAXT>
-__global__ void __launch_bounds__(st_threads(MAXT), st_blocks(MAXT))
+__global__ void __launch_bounds__(DR_THREADS, st_blocks(MAXT))
     draft_state_kernel(const DraftArgs p, const __grid_constant__ DraftMaps maps) {
-  constexpr int CT = st_cols(DV), TILES = DV / CT, NT = st_threads(MAXT);
-  constexpr int GROUPS = CT / 32, PARTS = st_parts(DK, DV, MAXT);
+  constexpr int CT = st_cols(DV), TILES = DV / CT, NT = DR_THREADS;
+  constexpr int GROUPS = CT / 32, PARTS = st_parts(DK, DV);
   constexpr int KS = DK / PARTS / 16;       // steps of 16 rows of a warp
   constexpr int RPT = 4 * KS;               // state rows of a thread (times 4 columns)
   constexpr int TEAMS = NT / CT;            // threads per column behind the sums
@@ -839,10 +871,10 @@ int prep_smem(int d_k, int r, int depth) {
   const int td = token_pad(depth);
   return (2 * td * (d_k + 8) + 4 * 2 * td * td + 3 * r * DR_MAX) * 4;
 }
-int state_smem(int d_k, int d_v, int max_t, int depth, int es) {
+int state_smem(int d_k, int d_v, int depth, int es) {
   const int rows = 4 * token_groups(depth), ct = st_cols(d_v);
   return (d_k * ct + depth * d_k + rows * ct + 2 * late_floats(ct, depth, es) +
-          st_parts(d_k, d_v, max_t) * 2 * rows * ct) * 4 +
+          st_parts(d_k, d_v) * 2 * rows * ct) * 4 +
          frag_bytes(d_k, token_groups(depth)) + 16 + 4 * (int)sizeof(DraftTile) + 1024;
 }
 
@@ -928,10 +960,10 @@ cudaError_t launch_state(const DraftArgs& a, cudaStream_t s) {
   cudaError_t e = draft_maps(&maps, a, st_cols(DV));
   if (e != cudaSuccess) return e;
   const int es = a.qkv_dtype == GDN_F32 ? 4 : 2;
-  const int bytes = state_smem(DK, DV, MAXT, a.rec.depth, es);
+  const int bytes = state_smem(DK, DV, a.rec.depth, es);
   static std::atomic<int> smem_set[64];
   // for the largest depth, so that the limit is set once
-  e = allow_smem(kern, state_smem(DK, DV, MAXT, MAXT, 4), smem_set);
+  e = allow_smem(kern, state_smem(DK, DV, MAXT, 4), smem_set);
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
   if (sms == 0) return cudaErrorInvalidDevice;
@@ -945,7 +977,7 @@ cudaError_t launch_state(const DraftArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(total < (int64_t)sms * per_sm ? total : (int64_t)sms * per_sm));
-  cfg.blockDim = dim3(st_threads(MAXT));
+  cfg.blockDim = dim3(DR_THREADS);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;
   cfg.attrs = attr;
