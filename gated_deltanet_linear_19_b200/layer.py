@@ -7,17 +7,21 @@ Holds the recurrent-state pool [n_slots, H_v, d_k, d_v] (fp32) and the conv-stat
   prefill: gdn_layer_prefill (front inside the chunked prefill) where it applies (d = 128,
            d_conv = 4, bf16 x and conv state, fp16 operands), else gdn_conv_step (fp16
            q/k/v, fp32 for the precise path) -> gdn_chunked_prefill
+  draft  : gdn_layer_draft (a speculative step that can be rolled back)
 Intermediate buffers are allocated through torch (cached per token count) and reused, so a
 steady-state step allocates nothing. All arithmetic runs in libgdn.so.
+
+GDNBlock puts the projections around it (gdn_linear): hidden state in, hidden state plus
+residual out, for the same three kinds of step.
 """
 from __future__ import annotations
 
 import torch
 
-from . import (DecodePipe, GDN_PREFILL_OUT_GATE, GDN_PREFILL_RECURRENT, GDN_PREFILL_SIMT, Dims,
-               chunked_prefill, conv_step, decode_workspace_size, draft_record,
-               draft_workspace_size, front_outputs, gated_norm, layer_decode, layer_decode_plan,
-               layer_draft, layer_prefill, prefill_workspace_size)
+from . import (DecodePipe, GDN_GATES_MIXED_BA, GDN_PREFILL_OUT_GATE, GDN_PREFILL_RECURRENT,
+               GDN_PREFILL_SIMT, Dims, OutGate, chunked_prefill, conv_step, decode_workspace_size,
+               draft_record, draft_workspace_size, front_outputs, gated_norm, layer_decode,
+               layer_decode_plan, layer_draft, layer_prefill, linear, prefill_workspace_size)
 
 
 class GDNLayer:
@@ -109,11 +113,13 @@ class GDNLayer:
 
     def _draft_ws(self, T: int, n_seqs: int, depth: int):
         need = draft_workspace_size(self.dims, T, n_seqs, depth)
-        ws = self._bufs.get("draft_ws")
-        if ws is None or ws.numel() < need:
-            ws = torch.empty(max(need, 1), dtype=torch.uint8, device=self.device)
-            self._bufs["draft_ws"] = ws
-        return ws
+        all_ws = self._bufs.setdefault("draft_ws", [])
+        if not all_ws or all_ws[-1].numel() < need:
+            # the smaller ones stay: a captured graph may still use them (at least doubling, they
+            # take no more than the last one together)
+            size = max(need, 2 * all_ws[-1].numel() if all_ws else 1)
+            all_ws.append(torch.empty(size, dtype=torch.uint8, device=self.device))
+        return all_ws[-1]
 
     def draft(self, x, a, b, cu_seqlens, slot_ids, accepted, record, *, reset=None, out=None,
               gate=None):
@@ -177,3 +183,62 @@ class GDNLayer:
         if gate is not None:
             gated_norm(self.dims, core_o, gate, o)
         return o
+
+
+class GDNBlock:
+    """The layer between hidden states: hidden [T, D] -> x, z, gates -> GDNLayer with its output
+    gate -> o w_out^T + residual [T, D].
+
+    w_x [conv_dim, D], w_z [H_v d_v, D] and w_out [D, H_v d_v] are bf16, as the hidden states and
+    the layer's outputs (o_dtype) are. w_gates [2 H_v, D] holds the beta/alpha rows in the order of the fused projection if the
+    layer's dims have GDN_GATES_MIXED_BA, else the H_v alpha rows and then the H_v beta rows.
+    norm_w [d_v] fp32 is the output gate's weight."""
+
+    def __init__(self, layer: GDNLayer, w_x, w_z, w_gates, norm_w, w_out, *, norm_eps=1e-6):
+        d = layer.dims
+        D = w_x.shape[1]
+        want = ((d.conv_dim, D), (d.H_v * d.d_v, D), (2 * d.H_v, D), (D, d.H_v * d.d_v))
+        for w, shape in zip((w_x, w_z, w_gates, w_out), want):
+            if tuple(w.shape) != shape or w.dtype != torch.bfloat16:
+                raise ValueError(f"gdn: a projection is {tuple(w.shape)} {w.dtype}, not {shape} "
+                                 "bf16")
+        if tuple(norm_w.shape) != (d.d_v,) or layer.o_dtype != torch.bfloat16:
+            raise ValueError("gdn: norm_w is [d_v] and the layer's o_dtype bf16")
+        put = lambda w: w.to(layer.device).contiguous()  # noqa: E731
+        self.layer, self.norm_eps = layer, float(norm_eps)
+        self.w_x, self.w_z, self.w_gates, self.w_out = (put(w) for w in (w_x, w_z, w_gates, w_out))
+        self.norm_w = put(norm_w.to(torch.float32))
+
+    def _project(self, hidden):
+        """x, a, b and the output gate of the hidden states."""
+        d = self.layer.dims
+        x, z = linear(hidden, self.w_x), linear(hidden, self.w_z)
+        gates = lambda w: linear(hidden, w, out_dtype=torch.float32)  # noqa: E731
+        if d.layout & GDN_GATES_MIXED_BA:
+            a, b = gates(self.w_gates).view(-1, d.H_k, 2 * (d.H_v // d.H_k)), None
+        else:
+            a, b = gates(self.w_gates[:d.H_v]), gates(self.w_gates[d.H_v:])
+        return x, a, b, OutGate(z.view(-1, d.H_v, d.d_v), self.norm_w, self.norm_eps)
+
+    def _finish(self, o, residual, out):
+        return linear(o.view(o.shape[0], -1), self.w_out, residual=residual, out=out)
+
+    def decode(self, hidden, slot_ids, *, residual=None, reset=None, out=None):
+        """One token for each of B sequences. out may be the residual."""
+        x, a, b, gate = self._project(hidden)
+        o = self.layer.decode(x, a, b, slot_ids, reset=reset, gate=gate)
+        return self._finish(o, residual, out)
+
+    def prefill(self, hidden, cu_seqlens, slot_ids, *, residual=None, reset=None, out=None):
+        """Packed sequences."""
+        x, a, b, gate = self._project(hidden)
+        o = self.layer.prefill(x, a, b, cu_seqlens, slot_ids, reset=reset, gate=gate)
+        return self._finish(o, residual, out)
+
+    def draft(self, hidden, cu_seqlens, slot_ids, accepted, record, *, residual=None, reset=None,
+              out=None):
+        """One speculative step (GDNLayer.draft)."""
+        x, a, b, gate = self._project(hidden)
+        o = self.layer.draft(x, a, b, cu_seqlens, slot_ids, accepted, record, reset=reset,
+                             gate=gate)
+        return self._finish(o, residual, out)

@@ -7,6 +7,9 @@ values, each rounded to half a step (2^-24 relative), through at most T + 1 depe
 element is off by at most gamma = (T + 2) (d_k + 2 T + 16) 2^-24 times the same recurrence run on
 absolute values (`bound`). An output in bf16 adds half its step, 2^-8 of the value. Errors of
 random sign stay far below that bound, so the relative L2 error is held to 1e-5 as well (fp32).
+The sums over d_k take 22 bits of each factor (two parts of 11): a product is off by at most
+3 2^-22 of itself, 12 of gamma's steps, and the matrix unit truncates its running sum d_k / 4 times,
+at most 2 steps each; gamma allows (T + 2) (d_k + 16) steps, more than d_k / 2 + 12.
 """
 import numpy as np
 import pytest
@@ -528,3 +531,67 @@ def test_results_do_not_depend_on_the_batch():
                        rec1, o1)
         assert torch.equal(o1, o[sl]) and torch.equal(alone[s.long()], state[s.long()])
     assert device_status() == 0
+
+
+@pytest.mark.parametrize("depth", [4, 7, 16])
+def test_many_sequences_equal_single_calls(depth):
+    """More tiles than blocks, ragged drafts with commits only, nothing at all, resets and skipped
+    sequences among them: every sequence gives the bits of a call of its own."""
+    dims = Dims(n_slots=220, H_k=2, H_v=6, d_k=128, d_v=128)
+    gen = torch.Generator().manual_seed(depth)
+    n = 200  # x 6 heads x 2 column tiles
+    state = torch.randn((220, 6, 128, 128), generator=gen).cuda()
+    alone = state.clone()
+    slots = torch.randperm(220, generator=gen)[:n].int().cuda()
+    slots[50], slots[120] = -1, slots[3]  # out of range, taken already: both are skipped
+    recs = [gdn.draft_record(dims, depth) for _ in range(2)]
+    lens0 = [depth] * n
+    q, k, v, g, beta, o = inputs(dims, sum(lens0), gen, torch.float16)
+    gdn.draft_step(dims, q, k, v, g, beta, state, slots, cu_of(lens0), None, recs[0], o)
+    assert device_status() == -2
+    for x, y in ((recs[1].n, recs[0].n), (recs[1].e, recs[0].e), (recs[1].k, recs[0].k),
+                 (recs[1].u, recs[0].u)):
+        x.copy_(y)
+    lens = [(7 * i) % (depth + 1) for i in range(n)]
+    acc = [(5 * i) % (depth + 1) if i % 3 else 0 for i in range(n)]
+    reset = torch.tensor([i % 11 == 4 for i in range(n)], dtype=torch.uint8).cuda()
+    q, k, v, g, beta, o = inputs(dims, sum(lens), gen, torch.float16)
+    gdn.draft_step(dims, q, k, v, g, beta, state, slots, cu_of(lens), i32(acc), recs[0], o,
+                   reset=reset)
+    assert device_status() == -2
+    o1, t0 = torch.full_like(o, float("nan")), 0
+    for i in range(n):
+        sl = slice(t0, t0 + lens[i])
+        t0 += lens[i]
+        if i in (50, 120):
+            assert torch.isnan(o[sl]).all()
+            continue
+        one = [t[sl].clone() for t in (q, k, v, g, beta, o1)]  # slices need not be 16-byte aligned
+        gdn.draft_step(dims, *one[:5], alone, slots[i:i + 1].clone(), cu_of([lens[i]]),
+                       i32([acc[i]]), recs[1], one[5], reset=reset[i:i + 1].clone())
+        o1[sl] = one[5]
+    assert device_status() == 0
+    assert torch.equal(o.nan_to_num(7.0), o1.nan_to_num(7.0)) and torch.equal(state, alone)
+    for x, y in ((recs[1].n, recs[0].n), (recs[1].e, recs[0].e), (recs[1].k, recs[0].k),
+                 (recs[1].u, recs[0].u)):
+        assert torch.equal(x, y)
+
+
+def test_scales_of_state_and_keys():
+    """States of 1e-12 to 1e12 and keys far from unit length: the parts of the column sums lose
+    nothing to the values' size."""
+    dims = Dims(n_slots=4, H_k=1, H_v=1, d_k=128, d_v=64)
+    gen = torch.Generator().manual_seed(21)
+    scale = torch.tensor([1e-12, 1.0, 1e6, 1e12])[:, None, None, None]
+    state = (torch.randn((4, 1, 128, 64), generator=gen) * scale).cuda()
+    rec = gdn.draft_record(dims, 3)
+    m = Model(dims, 3, state)
+    q, k, v, g, beta, o = inputs(dims, 12, gen, torch.float32)
+    k.mul_(torch.logspace(-3, 0, 12).cuda()[:, None, None])
+    gdn.draft_step(dims, q, k, v, g, beta, state, i32([0, 1, 2, 3]), cu_of([3] * 4), None, rec, o)
+    assert device_status() == 0
+    for n in range(4):
+        sl = slice(3 * n, 3 * n + 3)
+        ref, bnd = m.draft(n, *(f64(t)[sl] for t in (q, k, v, g, beta)))
+        near(f64(o)[sl], ref, bnd, 3, 128, f"o at {n}")
+        near(f64(rec.u)[n, :, :3], m.u[n, :, :3], m.ub[n, :, :3], 3, 128, f"u at {n}")
