@@ -14,21 +14,27 @@
 // so the state is read once, written at most once (only when something is committed), and the
 // column sums S^T [k, q] of all tokens come from one pass over it. The decays are running
 // products of numbers exp(g), never differences of cumulative logarithms, so gates of any size
-// (down to -inf) lose nothing. fp32 throughout: o, u and the state equal the token recurrence to
-// fp32 rounding.
+// (down to -inf) lose nothing. State, sums, u and o are fp32; the factors of the column sums count
+// with 22 bits (see draft_state_kernel).
 //
 // Two kernels, the second launched programmatically on the first:
 //  - draft_prep_kernel, one block per (key head, sequence): validity of the sequence; q and k
 //    (given, or from raw x: conv from the window behind the accepted tokens, SiLU, L2 norm), the
 //    gates, the tokens' dot products and the two T x T coefficient tables, the accepted keys of
 //    the old record and then the new record's keys, decays and inputs. What the second kernel
-//    needs goes to the workspace (a few KB per head, read from L2).
-//  - draft_state_kernel, HBM-bound, over tiles of up to 64 columns of one (value head, sequence):
-//    commit, column sums, the T-step triangular solve per column, o and the record's u. As many
-//    blocks as fit stay resident and take tiles in turn. A tile's inputs come by asynchronous
-//    copies (TMA for the state, bulk copies for the rest) that are started when the block has
+//    needs goes to the workspace (a few KB per head, read from L2). It moves little and is bound by
+//    the latency of its loads, so all of them are asked for before the first is waited for: 8.5 us
+//    at 64 sequences x 4 tokens with q and k given, 43 us at 128 x 0..8 from raw x (2048 blocks).
+//  - draft_state_kernel, over tiles of up to 64 columns of one (value head, sequence): commit,
+//    column sums, the T-step triangular solve per column, o and the record's u. As many blocks as
+//    fit stay resident and take tiles in turn. A tile's inputs come by asynchronous copies (TMA
+//    boxes for the state, v and u, bulk copies for the rest) that are started when the block has
 //    moved the tile before into registers, so that HBM works while the block computes; the first
-//    tile's state is asked for before the first kernel has finished.
+//    tile's state is asked for before the first kernel has finished. Measured on 64 sequences x 32
+//    heads of 128 x 128: 4 tokens each 41 us without and 59 with something to commit (the state's
+//    bytes alone: 20.5 and 41), 16 tokens 129 and 172 us. What bounds it: HBM up to about 4
+//    tokens, then the latency of a block's phases at 16, 12 and 8 warps per SM (depth 4, 8, 16;
+//    issue slots 34-44 % busy).
 // The keys of a record are shared by the column tiles and value heads of a key head, so they are
 // rewritten by the first kernel, which alone reads them; u belongs to one tile; the count n is
 // read by the first kernel and written by the second. Nothing is read and written by different
@@ -58,7 +64,8 @@ __host__ __device__ __forceinline__ int coef_size(int T) {
 }
 constexpr int DR_COEF = 2 * DR_MAX * DR_MAX + 3 * DR_MAX + 4;  // coef_size(DR_MAX)
 
-// A set of the state kernel's second inputs in shared memory (es: bytes of a v element), in floats.
+// A set of what the state kernel reads last of a tile, v and the coefficients, in shared memory (es:
+// bytes of a v element), in floats.
 __host__ __device__ __forceinline__ int late_floats(int ct, int depth, int es) {
   return token_groups(depth) * ct * es + (coef_size(depth) + 31) / 32 * 32;
 }
@@ -77,6 +84,12 @@ struct alignas(16) DraftHeader {
 // What the matrix unit leaves of an fp32 operand: it reads 1 + 8 + 10 bits (tf32) and drops the rest.
 __device__ __forceinline__ float tf32_rest(float x) {
   return x - __uint_as_float(__float_as_uint(x) & 0xffffe000u);
+}
+// x rounded to those bits (to nearest).
+__device__ __forceinline__ float tf32_round(float x) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+  return __uint_as_float(r);
 }
 // d += a b: a 16 x 8, b 8 x 8 in tf32, d fp32, in the warp's fragment layout.
 __device__ __forceinline__ void mma_tf32(float (&d)[4], float a0, float a1, float a2, float a3,
@@ -721,10 +734,12 @@ __global__ void __launch_bounds__(DR_THREADS, st_blocks(MAXT))
       const int ng = token_groups(T);
       if (mine) {
         // ---- column sums S^T k_t and S^T q_t of the warp's rows on the matrix unit, columns as M,
-        // vectors as N. An operand's first 11 bits go in as they are, the next 11 as a second
-        // operand; of their four products the one of both rests, 2^-22 of the whole, is left out.
-        // The large products and the others are summed apart: the adder cuts off what lies below
-        // its running sum's 24 bits.
+        // vectors as N. An operand's first 11 bits go in as one operand, what is left of it as a
+        // second (of which 11 bits count); of the four products that of both rests is left out: at
+        // most 2^-21 of the whole, and of either sign, since a key's rest is one of rounding. A
+        // product is within 2^-19 of itself, on average within 2^-22. Sums are fp32; the large
+        // products and the others are summed apart, because the adder cuts off what lies below its
+        // running sum's 24 bits.
         // One group of 4 tokens after another in a loop: unrolled over the groups, the code no longer
         // fits the instruction cache (one token per sequence, depth 16: 70.5 us).
 #pragma unroll 1
@@ -740,8 +755,9 @@ __global__ void __launch_bounds__(DR_THREADS, st_blocks(MAXT))
             // rows 2 k and 2 k + 1 of the thread; operand rows fq and fq + 8 are columns 4 fq + 2 mt
             // and 4 fq + 2 mt + 1
             const float4 x = s[2 * k], y = s[2 * k + 1];
-            const float2 b = f[k * 32];
-            const float2 br = make_float2(tf32_rest(b.x), tf32_rest(b.y));
+            const float2 full_b = f[k * 32];
+            const float2 b = make_float2(tf32_round(full_b.x), tf32_round(full_b.y));
+            const float2 br = make_float2(full_b.x - b.x, full_b.y - b.y);
             mma_tf32(hi[0], x.x, x.y, y.x, y.y, b);
             mma_tf32(hi[1], x.z, x.w, y.z, y.w, b);
             mma_tf32(lo[0], x.x, x.y, y.x, y.y, br);

@@ -337,8 +337,9 @@ typedef struct gdn_draft_record {
  * Sequence n commits the first accepted[n] tokens of its slot's record to state[slot_ids[n]],
  * then runs its cu_seqlens[n+1] - cu_seqlens[n] new tokens (0 to depth) from that state, writes
  * their outputs to o and makes them the slot's record (rows behind the last token keep their
- * values). A sequence with no new tokens only commits. The arithmetic is fp32; o and the record
- * equal the token recurrence up to fp32 rounding (o rounded once to o_dtype).
+ * values). A sequence with no new tokens only commits. State, sums, o and the record are fp32 (o
+ * rounded once to o_dtype); in the sums over d_k of state times key or query each factor counts
+ * with 22 bits, a product within 2^-19 of itself (2^-22 on average).
  *   q, k [T_total][H_k][d_k], v [T_total][H_v][d_v] (qkv_dtype F32, F16 or BF16), g, beta
  *       [T_total][H_v] fp32, g of any size (-inf clears the past)
  *   state, slot_ids, reset: as gdn_decode_step (reset[n] != 0: zero state, the record is dropped
@@ -347,7 +348,8 @@ typedef struct gdn_draft_record {
  *       equal n_seqs)
  *   accepted [n_seqs] int32, or NULL meaning all zero
  *   o [T_total][H_v][d_v], o_dtype F32 or BF16
- *   workspace: at least gdn_draft_workspace_size() bytes, 16-byte aligned, overwritten
+ *   workspace: at least gdn_draft_workspace_size() bytes, 16-byte aligned, overwritten; of one
+ *       call at a time (calls that may run at the same time need one each)
  * A sequence with more than depth new tokens, with accepted[n] negative or above the record's
  * count, or with a bad or repeated slot id is skipped as a whole (state, record and outputs
  * untouched) and GDN_EINVAL or GDN_ESLOT is recorded. H_v / H_k at most 256

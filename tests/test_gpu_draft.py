@@ -7,9 +7,10 @@ values, each rounded to half a step (2^-24 relative), through at most T + 1 depe
 element is off by at most gamma = (T + 2) (d_k + 2 T + 16) 2^-24 times the same recurrence run on
 absolute values (`bound`). An output in bf16 adds half its step, 2^-8 of the value. Errors of
 random sign stay far below that bound, so the relative L2 error is held to 1e-5 as well (fp32).
-The sums over d_k take 22 bits of each factor (two parts of 11): a product is off by at most
-3 2^-22 of itself, 12 of gamma's steps, and the matrix unit truncates its running sum d_k / 4 times,
-at most 2 steps each; gamma allows (T + 2) (d_k + 16) steps, more than d_k / 2 + 12.
+The sums over d_k take each factor in two parts of 11 bits and leave out the product of both second
+parts: a product is off by less than 2^-21 + 2^-22 + 2^-21 < 2^-19 of itself, 32 of gamma's steps,
+and the matrix unit truncates its running sum d_k / 8 times, at most 2 steps each. gamma allows
+(T + 2) (d_k + 16) steps for each dependent pass, more than the d_k / 4 + 32 that these take.
 """
 import numpy as np
 import pytest
