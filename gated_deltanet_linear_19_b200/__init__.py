@@ -316,73 +316,16 @@ def gated_norm(dims: Dims, o, gate: OutGate, out=None, *, stream=None):
     return out
 
 
-# The current stream of a device as a raw handle, without building a Stream object (2 us per call,
-# as much as a small kernel).
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _ptr(t, dev):
-    """Address of a contiguous tensor on CUDA device `dev` (None stays None)."""
-    if t is None:
-        return None
-    if t.get_device() != dev:
-        raise ValueError("gdn: tensors must live on one CUDA device")
-    if not t.is_contiguous():
-        raise ValueError("gdn: tensors must be contiguous")
-    return t.data_ptr()
-
-
-def _call(fn, where, dev, stream, *args):
-    """fn(*args, stream) with device `dev` current, on the given stream or the device's current
-    one."""
-    s = _raw_stream(dev) if stream is None else stream.cuda_stream
-    if dev == torch.cuda.current_device():
-        rc = fn(*args, s)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, s)
-    if rc != GDN_OK:
-        raise GdnError(rc, where)
-
-
 def linear(x, w, *, bias=None, act="none", residual=None, out=None, out_dtype=None, stream=None):
     """gdn_linear: out = act(x w^T + bias) + residual. x [M, K] and w [N, K] bf16 or fp16 with
     contiguous rows (any row stride that is a multiple of 8 elements), bias [N] fp32, act "none",
     "silu", "gelu" or "sigmoid", residual and out [M, N] with contiguous rows (out may be the
     residual). out is allocated (of out_dtype, x's type by default) if not given."""
-    M, K = x.shape
-    N, k_w = w.shape
-    dev, dtype = x.get_device(), x.dtype
-    if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or dtype, device=x.device)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError("gdn: out is not of out_dtype")
-    if dev < 0 or w.get_device() != dev or out.get_device() != dev or w.dtype != dtype or \
-            k_w != K or out.shape != (M, N):
-        raise ValueError("gdn: linear takes x [M, K], w [N, K] of one type and out [M, N] on one "
-                         "CUDA device")
-    b = r = None
-    r_code, ldr = GDN_F32, N
-    if bias is not None:
-        if bias.shape != (N,) or bias.dtype != torch.float32:
-            raise ValueError("gdn: bias is a contiguous fp32 [N]")
-        b = _ptr(bias, dev)
-    if residual is not None:
-        if residual.shape != (M, N) or residual.get_device() != dev:
-            raise ValueError("gdn: residual is [M, N]")
-        r, r_code, ldr = residual.data_ptr(), DTYPE_CODE[residual.dtype], _row_stride(residual)
-    _call(_lib.load().gdn_linear, "gdn_linear", dev, stream, x.data_ptr(), _row_stride(x),
-          w.data_ptr(), _row_stride(w), DTYPE_CODE[dtype], b, _ACT[act], r, r_code, ldr,
-          out.data_ptr(), DTYPE_CODE[out.dtype], _row_stride(out), M, N, K)
-    return out
-
-
-def _row_stride(t):
-    """Elements between the rows of a 2-D tensor whose rows are contiguous."""
-    s0, s1 = t.stride()
-    if s1 != 1 and t.shape[1] > 1:
-        raise ValueError("gdn: rows must be contiguous")
-    return s0 if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
+    y = _lib.fast().linear(x, w, bias, _ACT[act], residual, out, out_dtype,
+                           None if stream is None else stream.cuda_stream)
+    if type(y) is int:
+        raise GdnError(y, "gdn_linear")
+    return y
 
 
 @dataclass(frozen=True)
@@ -401,20 +344,6 @@ class DraftRecord:
     def depth(self) -> int:
         return self.e.shape[2]
 
-    def _c(self, dims: Dims, dev: int, conv_dtype=None):
-        n, e, k, u, x = self.n, self.e, self.k, self.u, self.x
-        s, hv, d = dims.n_slots, dims.H_v, e.shape[2]
-        if (n.shape != (s,) or e.shape != (s, hv, d) or k.shape != (s, dims.H_k, d, dims.d_k)
-                or u.shape != (s, hv, d, dims.d_v) or n.dtype != torch.int32
-                or not e.dtype == k.dtype == u.dtype == torch.float32):
-            raise ValueError("gdn: draft record does not fit the dims")
-        if conv_dtype is None:
-            x = None
-        elif x is None or x.dtype != conv_dtype or x.shape != (s, d, dims.conv_dim):
-            raise ValueError("gdn: draft record's x does not fit the dims and conv state")
-        return ctypes.byref(_lib.GdnDraftRecord(d, _ptr(n, dev), _ptr(e, dev), _ptr(k, dev),
-                                                _ptr(u, dev), _ptr(x, dev)))
-
 
 def draft_record(dims: Dims, depth: int, *, conv_dtype=torch.bfloat16,
                  device="cuda") -> DraftRecord:
@@ -431,42 +360,17 @@ def draft_workspace_size(dims: Dims, T_total: int, n_seqs: int, depth: int) -> i
                                                     int(n_seqs), int(depth)))
 
 
-def _draft_seqs(slot_ids, cu_seqlens, accepted, reset):
-    """The number of sequences, after checking the per-sequence arrays against it."""
-    n = slot_ids.numel()
-    if slot_ids.dtype != torch.int32 or \
-            (accepted is not None and (accepted.dtype != torch.int32 or accepted.numel() != n)) or \
-            (cu_seqlens is not None and (cu_seqlens.dtype != torch.int32
-                                         or cu_seqlens.numel() != n + 1)) or \
-            (reset is not None and (reset.element_size() != 1 or reset.numel() != n)):
-        raise ValueError("gdn: slot_ids, accepted [n], cu_seqlens [n + 1] are int32 and reset [n] "
-                         "holds bytes")
-    return n
-
-
-def _draft_ws(lib, cdims, T, n_seqs, depth, workspace, device):
-    if workspace is None:
-        need = lib.gdn_draft_workspace_size(cdims, T, n_seqs, depth)
-        return torch.empty(need or 1, dtype=torch.uint8, device=device), need
-    return workspace, workspace.numel() * workspace.element_size()
-
-
 def draft_step(dims: Dims, q, k, v, g, beta, state, slot_ids, cu_seqlens, accepted,
                record: DraftRecord, o, *, reset=None, workspace=None, stream=None):
     """gdn_draft_step: commit the accepted tokens of each slot's record, then run the new drafted
     tokens without advancing the state (o written, record replaced). cu_seqlens=None: one new
     token per sequence; accepted=None: nothing is committed. Allocates the workspace if not
     given."""
-    lib, dev = _lib.load(), state.get_device()
-    cdims = ctypes.byref(dims.c())
-    T = q.shape[0]
-    n_seqs = _draft_seqs(slot_ids, cu_seqlens, accepted, reset)
-    rec = record._c(dims, dev)
-    ws, ws_bytes = _draft_ws(lib, cdims, T, n_seqs, record.depth, workspace, state.device)
-    _call(lib.gdn_draft_step, "gdn_draft_step", dev, stream, cdims, _ptr(q, dev), _ptr(k, dev),
-          _ptr(v, dev), _code(q), _ptr(g, dev), _ptr(beta, dev), _ptr(state, dev),
-          _ptr(slot_ids, dev), _ptr(cu_seqlens, dev), _ptr(reset, dev), _ptr(accepted, dev),
-          n_seqs, T, rec, _ptr(o, dev), _code(o), _ptr(ws, dev), ws_bytes)
+    rc = _lib.fast().draft_step(dims, q, k, v, g, beta, state, slot_ids, cu_seqlens, accepted,
+                                record, o, reset, workspace,
+                                None if stream is None else stream.cuda_stream)
+    if rc is not None:
+        raise GdnError(rc, "gdn_draft_step")
 
 
 def layer_draft(dims: Dims, x, conv_w, conv_state, cu_seqlens, slot_ids, accepted, a, b, A_log,
@@ -475,21 +379,12 @@ def layer_draft(dims: Dims, x, conv_w, conv_state, cu_seqlens, slot_ids, accepte
     """gdn_layer_draft: draft_step from raw projections x [T, conv_dim], the convolution's window
     rolled to the accepted tokens, with the optional OutGate. Allocates the workspace if not
     given."""
-    lib, dev = _lib.load(), state.get_device()
-    if q_scale is None:
-        q_scale = dims.d_k ** -0.5
-    cdims = ctypes.byref(dims.c())
-    T = x.shape[0]
-    n_seqs = _draft_seqs(slot_ids, cu_seqlens, accepted, reset)
-    conv_dtype = conv_state.dtype if conv_state is not None else None
-    rec = record._c(dims, dev, conv_dtype)
-    ws, ws_bytes = _draft_ws(lib, cdims, T, n_seqs, record.depth, workspace, state.device)
-    _call(lib.gdn_layer_draft, "gdn_layer_draft", dev, stream, cdims, _ptr(x, dev), _code(x),
-          _ptr(conv_w, dev), _ptr(conv_state, dev),
-          DTYPE_CODE[conv_dtype] if conv_dtype is not None else GDN_F32, _ptr(cu_seqlens, dev),
-          _ptr(slot_ids, dev), _ptr(reset, dev), _ptr(accepted, dev), n_seqs, T, _ptr(a, dev),
-          _ptr(b, dev), _ptr(A_log, dev), _ptr(dt_bias, dev), eps, q_scale, _ptr(state, dev), rec,
-          _ptr(o, dev), _code(o), _ptr(ws, dev), ws_bytes, _gate(gate))
+    rc = _lib.fast().layer_draft(dims, x, conv_w, conv_state, cu_seqlens, slot_ids, accepted, a, b,
+                                 A_log, dt_bias, state, record, o, eps,
+                                 dims.d_k ** -0.5 if q_scale is None else q_scale, reset,
+                                 workspace, gate, None if stream is None else stream.cuda_stream)
+    if rc is not None:
+        raise GdnError(rc, "gdn_layer_draft")
 
 
 def prefill_workspace_size(dims: Dims, T_total: int, n_seqs: int, chunk: int = 64,

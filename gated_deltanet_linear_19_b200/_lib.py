@@ -161,3 +161,26 @@ def load(path: str | None = None):
         lib.gdn_abi_version.restype = I32
         _lib = lib
         return lib
+
+
+_fast = None
+
+
+def fast():
+    """The compiled marshalling of the shortest calls, bound to the loaded library. Raises if it
+    is not built."""
+    global _fast
+    if _fast is None:
+        lib = load()
+        try:
+            import torch  # noqa: F401  (the module needs its libraries)
+
+            from . import _fast as module
+        except ImportError as e:
+            raise RuntimeError("_fast.so not found or not loadable; build it with `python -m "
+                               "gated_deltanet_linear_19_b200.build`") from e
+        address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
+        module.bind(address(lib.gdn_linear), address(lib.gdn_draft_step),
+                    address(lib.gdn_layer_draft), address(lib.gdn_draft_workspace_size))
+        _fast = module
+    return _fast

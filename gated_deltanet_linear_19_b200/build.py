@@ -1,4 +1,5 @@
-"""Build libgdn.so in-tree with nvcc for sm_100a (one object per .cu, compiled in parallel).
+"""Build libgdn.so in-tree with nvcc for sm_100a (one object per .cu, compiled in parallel) and
+_fast.so, the Python marshalling of the shortest calls, with g++ against torch's headers.
 
 Usage: python -m gated_deltanet_linear_19_b200.build [--force] [--verbose-ptxas]
 """
@@ -15,6 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
+FAST = os.path.join(PKG, "_fast.so")
+FAST_SRC = os.path.join(CSRC, "binding.cpp")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -42,7 +45,32 @@ def needs_build() -> bool:
     return any(os.path.getmtime(f) > t for f in sources() + _deps() + [__file__])
 
 
+def build_fast(force: bool = False) -> str:
+    header = os.path.join(ROOT, "include", "gdn.h")
+    if not force and os.path.exists(FAST) and os.path.getmtime(FAST) >= max(
+            os.path.getmtime(f) for f in (FAST_SRC, header, __file__)):
+        return FAST
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    inc = [os.path.join(base, "include"),
+           os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"],
+           os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
+    tmp = FAST + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", FAST_SRC, "-o", tmp]
+    cmd += ["-I" + d for d in inc]
+    cmd += ["-L" + os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_python"]
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, FAST)
+    return FAST
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    build_fast(force)
     if not force and not needs_build():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

@@ -1,0 +1,403 @@
+// Python calls of gdn_linear, gdn_draft_step and gdn_layer_draft: argument checks and marshalling
+// only. These calls are as short as 4 to 10 us on the GPU, where building their arguments in Python
+// and passing them through ctypes took 5 to 11 us of host time; here it takes under 1 us.
+// Functions return the tensor (linear) or None, or the library's status code as an int; they raise
+// ValueError for arguments that the library cannot check itself (shapes, types, devices).
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <optional>
+#include <stdexcept>
+
+#include "../../include/gdn.h"
+
+namespace {
+
+decltype(&gdn_linear) p_linear = nullptr;
+decltype(&gdn_draft_step) p_draft_step = nullptr;
+decltype(&gdn_layer_draft) p_layer_draft = nullptr;
+decltype(&gdn_draft_workspace_size) p_draft_workspace = nullptr;
+
+struct Refused : std::runtime_error {
+  using std::runtime_error::runtime_error;
+};
+void need(bool ok, const char* what) {
+  if (!ok) throw Refused(what);
+}
+
+// A tensor argument, or null for None.
+const at::Tensor* tensor(PyObject* o) {
+  if (o == Py_None) return nullptr;
+  need(THPVariable_Check(o), "gdn: a tensor is expected");
+  return &THPVariable_Unpack(o);
+}
+const at::Tensor& must(const at::Tensor* t) {
+  need(t != nullptr, "gdn: a required tensor is missing");
+  return *t;
+}
+// Address of a contiguous tensor on CUDA device `dev` (null stays null).
+void* ptr(const at::Tensor* t, int dev) {
+  if (!t) return nullptr;
+  need(t->is_cuda() && t->get_device() == dev, "gdn: tensors must live on one CUDA device");
+  need(t->is_contiguous(), "gdn: tensors must be contiguous");
+  return t->data_ptr();
+}
+template <typename T>
+T* ptr_as(const at::Tensor* t, int dev) {
+  return static_cast<T*>(ptr(t, dev));
+}
+int code(at::ScalarType t) {
+  switch (t) {
+    case at::kFloat: return GDN_F32;
+    case at::kBFloat16: return GDN_BF16;
+    case at::kHalf: return GDN_F16;
+    default: throw Refused("gdn: tensors are fp32, bf16 or fp16");
+  }
+}
+// `n` values of `type` (a missing tensor passes: the library decides whether it may be missing).
+void holds(const at::Tensor* t, int64_t n, at::ScalarType type, const char* what) {
+  need(!t || (t->numel() == n && t->scalar_type() == type), what);
+}
+bool shaped(const at::Tensor& t, std::initializer_list<int64_t> s) {
+  return t.sizes() == at::IntArrayRef(s.begin(), s.size());
+}
+
+// An attribute of a Python object, as a new reference that ends with this object.
+struct Attr {
+  PyObject* o;
+  Attr(PyObject* from, PyObject* name) : o(PyObject_GetAttr(from, name)) {
+    if (!o) throw std::logic_error("python");  // the Python error is set
+  }
+  ~Attr() { Py_DECREF(o); }
+  Attr(const Attr&) = delete;
+  int as_int() const {
+    const long v = PyLong_AsLong(o);
+    if (v == -1 && PyErr_Occurred()) throw std::logic_error("python");
+    need(v >= INT32_MIN && v <= INT32_MAX, "gdn: a dimension is out of range");
+    return static_cast<int>(v);
+  }
+};
+double as_double(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw std::logic_error("python");
+  return v;
+}
+
+enum Name { N_SLOTS, H_K, H_V, D_K, D_V, D_CONV, LAYOUT, R_N, R_E, R_K, R_U, R_X, G_Z, G_W, G_EPS,
+            N_NAMES };
+PyObject* names[N_NAMES];
+
+gdn_dims dims_of(PyObject* o) {
+  gdn_dims d{};
+  d.n_slots = Attr(o, names[N_SLOTS]).as_int();
+  d.H_k = Attr(o, names[H_K]).as_int();
+  d.H_v = Attr(o, names[H_V]).as_int();
+  d.d_k = Attr(o, names[D_K]).as_int();
+  d.d_v = Attr(o, names[D_V]).as_int();
+  d.d_conv = Attr(o, names[D_CONV]).as_int();
+  d.layout = Attr(o, names[LAYOUT]).as_int();
+  return d;
+}
+int64_t conv_dim(const gdn_dims& d) {
+  return 2LL * d.H_k * d.d_k + static_cast<int64_t>(d.H_v) * d.d_v;
+}
+
+// Device and stream of a call. A stream given by its handle becomes current, so that what is
+// allocated here belongs to it; without one it is the device's current stream.
+struct Where {
+  std::optional<c10::cuda::CUDAStreamGuard> on_stream;
+  std::optional<c10::cuda::CUDAGuard> on_device;
+  gdn_stream_t stream;
+  Where(int dev, PyObject* handle) {
+    cudaStream_t s;
+    if (handle != Py_None) {
+      s = static_cast<cudaStream_t>(PyLong_AsVoidPtr(handle));
+      if (!s && PyErr_Occurred()) throw std::logic_error("python");
+      on_stream.emplace(c10::cuda::getStreamFromExternal(s, static_cast<c10::DeviceIndex>(dev)));
+    } else {
+      on_device.emplace(static_cast<c10::DeviceIndex>(dev));
+      s = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
+    }
+    stream = reinterpret_cast<gdn_stream_t>(s);
+  }
+};
+
+PyObject* status(int rc) {
+  if (rc == GDN_OK) Py_RETURN_NONE;
+  return PyLong_FromLong(rc);
+}
+
+template <typename F>
+PyObject* guarded(F f) {
+  try {
+    return f();
+  } catch (const Refused& e) {
+    PyErr_SetString(PyExc_ValueError, e.what());
+  } catch (const std::logic_error& e) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (const std::exception& e) {  // c10::Error: out of memory and the like
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  return nullptr;
+}
+
+// ------------------------------------------------------------------------------------- linear
+// Elements between the rows of a 2-D tensor whose rows are contiguous.
+int64_t row_stride(const at::Tensor& t) {
+  need(t.size(1) <= 1 || t.stride(1) == 1, "gdn: rows must be contiguous");
+  return t.size(0) > 1 ? t.stride(0) : (t.size(1) + 7) / 8 * 8;
+}
+
+// linear(x, w, bias, act, residual, out, out_dtype, stream)
+PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    need(n == 8, "gdn: linear takes 8 arguments");
+    const at::Tensor &x = must(tensor(a[0])), &w = must(tensor(a[1]));
+    const at::Tensor *bias = tensor(a[2]), *res = tensor(a[4]), *given = tensor(a[5]);
+    const long act = PyLong_AsLong(a[3]);
+    need(x.dim() == 2 && w.dim() == 2, "gdn: linear takes x [M, K] and w [N, K]");
+    const int64_t M = x.size(0), K = x.size(1), N = w.size(0);
+    const int dev = x.is_cuda() ? x.get_device() : -1;
+    at::ScalarType type = x.scalar_type();
+    if (a[6] != Py_None) {
+      need(THPDtype_Check(a[6]), "gdn: out_dtype is a torch dtype");
+      type = reinterpret_cast<THPDtype*>(a[6])->scalar_type;
+      need(!given || given->scalar_type() == type, "gdn: out is not of out_dtype");
+    }
+    need(dev >= 0 && w.is_cuda() && w.get_device() == dev && w.scalar_type() == x.scalar_type() &&
+             w.size(1) == K &&
+             (!given || (given->is_cuda() && given->get_device() == dev && shaped(*given, {M, N}))) &&
+             N <= INT32_MAX && K <= INT32_MAX,
+         "gdn: linear takes x [M, K], w [N, K] of one type and out [M, N] on one CUDA device");
+    need(!bias || (shaped(*bias, {N}) && bias->scalar_type() == at::kFloat),
+         "gdn: bias is a contiguous fp32 [N]");
+    need(!res || (shaped(*res, {M, N}) && res->is_cuda() && res->get_device() == dev),
+         "gdn: residual is [M, N] on x's device");
+    Where where(dev, a[7]);
+    at::Tensor made;
+    if (!given) made = at::empty({M, N}, x.options().dtype(type));
+    const at::Tensor& out = given ? *given : made;
+    const int xc = code(x.scalar_type()), oc = code(out.scalar_type());
+    const int rc_type = res ? code(res->scalar_type()) : GDN_F32;
+    const float* b = ptr_as<const float>(bias, dev);
+    const int64_t ldx = row_stride(x), ldw = row_stride(w), ldo = row_stride(out);
+    const int64_t ldr = res ? row_stride(*res) : N;
+    const void *xp = x.data_ptr(), *wp = w.data_ptr(), *rp = res ? res->data_ptr() : nullptr;
+    void* op = out.data_ptr();
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = p_linear(xp, ldx, wp, ldw, xc, b, static_cast<int32_t>(act), rp, rc_type, ldr, op, oc, ldo,
+                  M, static_cast<int32_t>(N), static_cast<int32_t>(K), where.stream);
+    Py_END_ALLOW_THREADS
+    if (rc != GDN_OK) return PyLong_FromLong(rc);
+    if (given) return Py_NewRef(a[5]);
+    return THPVariable_Wrap(made);
+  });
+}
+
+// -------------------------------------------------------------------------------- draft steps
+struct Record {
+  Attr n, e, k, u, x;
+  gdn_draft_record c{};
+  // conv: the conv state's type, or none (then x is not used)
+  Record(PyObject* o, const gdn_dims& d, int dev, std::optional<at::ScalarType> conv)
+      : n(o, names[R_N]), e(o, names[R_E]), k(o, names[R_K]), u(o, names[R_U]), x(o, names[R_X]) {
+    const at::Tensor &tn = must(tensor(n.o)), &te = must(tensor(e.o)), &tk = must(tensor(k.o)),
+                     &tu = must(tensor(u.o));
+    const at::Tensor* tx = tensor(x.o);
+    need(te.dim() == 3, "gdn: draft record does not fit the dims");
+    const int64_t s = d.n_slots, depth = te.size(2);
+    need(shaped(tn, {s}) && shaped(te, {s, d.H_v, depth}) && shaped(tk, {s, d.H_k, depth, d.d_k}) &&
+             shaped(tu, {s, d.H_v, depth, d.d_v}) && tn.scalar_type() == at::kInt &&
+             te.scalar_type() == at::kFloat && tk.scalar_type() == at::kFloat &&
+             tu.scalar_type() == at::kFloat && depth <= INT32_MAX,
+         "gdn: draft record does not fit the dims");
+    if (!conv) tx = nullptr;
+    need(!conv || (tx && tx->scalar_type() == *conv && shaped(*tx, {s, depth, conv_dim(d)})),
+         "gdn: draft record's x does not fit the dims and conv state");
+    c.depth = static_cast<int32_t>(depth);
+    c.n = ptr_as<int32_t>(&tn, dev);
+    c.e = ptr_as<float>(&te, dev);
+    c.k = ptr_as<float>(&tk, dev);
+    c.u = ptr_as<float>(&tu, dev);
+    c.x = ptr(tx, dev);
+  }
+};
+
+// The per-sequence arrays and the workspace of a draft step.
+struct Sequences {
+  int n;
+  const int32_t *slots, *cu, *accepted;
+  const uint8_t* reset;
+  at::Tensor made;
+  void* ws;
+  size_t ws_bytes;
+  Sequences(const at::Tensor& s, const at::Tensor* c, const at::Tensor* acc, const at::Tensor* rst,
+            const at::Tensor* workspace, const gdn_dims& d, int64_t T, int depth, int dev) {
+    const int64_t count = s.numel();
+    need(count <= INT32_MAX && s.scalar_type() == at::kInt &&
+             (!acc || (acc->scalar_type() == at::kInt && acc->numel() == count)) &&
+             (!c || (c->scalar_type() == at::kInt && c->numel() == count + 1)) &&
+             (!rst || (rst->element_size() == 1 && rst->numel() == count)),
+         "gdn: slot_ids, accepted [n], cu_seqlens [n + 1] are int32 and reset [n] holds bytes");
+    n = static_cast<int>(count);
+    slots = ptr_as<const int32_t>(&s, dev);
+    cu = ptr_as<const int32_t>(c, dev);
+    accepted = ptr_as<const int32_t>(acc, dev);
+    reset = ptr_as<const uint8_t>(rst, dev);
+    if (workspace) {
+      ws = ptr(workspace, dev);
+      ws_bytes = workspace->nbytes();
+    } else {
+      ws_bytes = p_draft_workspace(&d, T, n, depth);
+      made = at::empty({static_cast<int64_t>(ws_bytes ? ws_bytes : 1)},
+                       s.options().dtype(at::kByte));
+      ws = made.data_ptr();
+    }
+  }
+};
+
+// draft_step(dims, q, k, v, g, beta, state, slot_ids, cu_seqlens, accepted, record, o, reset,
+//            workspace, stream)
+PyObject* draft_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    need(n == 15, "gdn: draft_step takes 15 arguments");
+    const gdn_dims d = dims_of(a[0]);
+    const at::Tensor &q = must(tensor(a[1])), &k = must(tensor(a[2])), &v = must(tensor(a[3])),
+                     &state = must(tensor(a[6])), &o = must(tensor(a[11]));
+    const at::Tensor *g = tensor(a[4]), *beta = tensor(a[5]);
+    need(q.dim() >= 1 && state.is_cuda(), "gdn: tensors must live on one CUDA device");
+    const int64_t T = q.size(0);
+    const int dev = state.get_device();
+    need(k.scalar_type() == q.scalar_type() && v.scalar_type() == q.scalar_type() &&
+             q.numel() == T * d.H_k * d.d_k && k.numel() == q.numel() &&
+             v.numel() == T * d.H_v * d.d_v && o.numel() == v.numel(),
+         "gdn: q, k [T, H_k, d_k] and v [T, H_v, d_v] are of one type, o [T, H_v, d_v]");
+    holds(g, T * d.H_v, at::kFloat, "gdn: g and beta are fp32 [T, H_v]");
+    holds(beta, T * d.H_v, at::kFloat, "gdn: g and beta are fp32 [T, H_v]");
+    holds(&state, static_cast<int64_t>(d.n_slots) * d.H_v * d.d_k * d.d_v, at::kFloat,
+          "gdn: state is fp32 [n_slots, H_v, d_k, d_v]");
+    Where where(dev, a[14]);
+    const Record rec(a[10], d, dev, std::nullopt);
+    const Sequences s(must(tensor(a[7])), tensor(a[8]), tensor(a[9]), tensor(a[12]), tensor(a[13]),
+                      d, T, rec.c.depth, dev);
+    const int qc = code(q.scalar_type()), oc = code(o.scalar_type());
+    const void *qp = ptr(&q, dev), *kp = ptr(&k, dev), *vp = ptr(&v, dev);
+    const float *gp = ptr_as<const float>(g, dev), *bp = ptr_as<const float>(beta, dev);
+    float* sp = ptr_as<float>(&state, dev);
+    void* op = ptr(&o, dev);
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = p_draft_step(&d, qp, kp, vp, qc, gp, bp, sp, s.slots, s.cu, s.reset, s.accepted, s.n, T,
+                      &rec.c, op, oc, s.ws, s.ws_bytes, where.stream);
+    Py_END_ALLOW_THREADS
+    return status(rc);
+  });
+}
+
+// layer_draft(dims, x, conv_w, conv_state, cu_seqlens, slot_ids, accepted, a, b, A_log, dt_bias,
+//             state, record, o, eps, q_scale, reset, workspace, gate, stream)
+PyObject* layer_draft(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    need(n == 20, "gdn: layer_draft takes 20 arguments");
+    const gdn_dims d = dims_of(a[0]);
+    const at::Tensor &x = must(tensor(a[1])), &state = must(tensor(a[11])), &o = must(tensor(a[13]));
+    const at::Tensor *cw = tensor(a[2]), *cs = tensor(a[3]), *fa = tensor(a[7]), *fb = tensor(a[8]);
+    const at::Tensor *al = tensor(a[9]), *dt = tensor(a[10]);
+    need(x.dim() >= 1 && state.is_cuda(), "gdn: tensors must live on one CUDA device");
+    const int64_t T = x.size(0), cd = conv_dim(d);
+    const int dev = state.get_device();
+    need(x.numel() == T * cd && o.numel() == T * d.H_v * d.d_v,
+         "gdn: x is [T, conv_dim], o [T, H_v, d_v]");
+    holds(cw, cd * d.d_conv, at::kFloat, "gdn: conv_w is fp32 [conv_dim, d_conv]");
+    need(!cs || cs->numel() == static_cast<int64_t>(d.n_slots) * (d.d_conv - 1) * cd,
+         "gdn: conv_state is [n_slots, d_conv - 1, conv_dim]");
+    holds(fa, T * d.H_v * ((d.layout & GDN_GATES_MIXED_BA) ? 2 : 1), at::kFloat,
+          "gdn: a and b are fp32 [T, H_v] (a alone [T, H_k, 2 r] for the fused projection)");
+    holds(fb, T * d.H_v, at::kFloat, "gdn: b is fp32 [T, H_v]");
+    holds(al, d.H_v, at::kFloat, "gdn: A_log and dt_bias are fp32 [H_v]");
+    holds(dt, d.H_v, at::kFloat, "gdn: A_log and dt_bias are fp32 [H_v]");
+    holds(&state, static_cast<int64_t>(d.n_slots) * d.H_v * d.d_k * d.d_v, at::kFloat,
+          "gdn: state is fp32 [n_slots, H_v, d_k, d_v]");
+    Where where(dev, a[19]);
+    const Record rec(a[12], d, dev,
+                     cs ? std::optional<at::ScalarType>(cs->scalar_type()) : std::nullopt);
+    const Sequences s(must(tensor(a[5])), tensor(a[4]), tensor(a[6]), tensor(a[16]), tensor(a[17]),
+                      d, T, rec.c.depth, dev);
+    gdn_out_gate gate{};
+    const gdn_out_gate* gp = nullptr;
+    std::optional<Attr> z, nw;
+    if (a[18] != Py_None) {
+      z.emplace(a[18], names[G_Z]);
+      nw.emplace(a[18], names[G_W]);
+      const at::Tensor &tz = must(tensor(z->o)), &tw = must(tensor(nw->o));
+      need(tz.numel() == o.numel() && tw.numel() == d.d_v && tw.scalar_type() == at::kFloat,
+           "gdn: the gate's z is [T, H_v, d_v], its norm_w fp32 [d_v]");
+      gate.z = ptr(&tz, dev);
+      gate.z_dtype = code(tz.scalar_type());
+      gate.norm_w = ptr_as<const float>(&tw, dev);
+      gate.eps = static_cast<float>(as_double(Attr(a[18], names[G_EPS]).o));
+      gp = &gate;
+    }
+    const float eps = static_cast<float>(as_double(a[14]));
+    const float q_scale = static_cast<float>(as_double(a[15]));
+    const int xc = code(x.scalar_type()), oc = code(o.scalar_type());
+    const int cc = cs ? code(cs->scalar_type()) : GDN_F32;
+    const void* xp = ptr(&x, dev);
+    const float *cwp = ptr_as<const float>(cw, dev), *ap = ptr_as<const float>(fa, dev),
+                *bp = ptr_as<const float>(fb, dev), *alp = ptr_as<const float>(al, dev),
+                *dtp = ptr_as<const float>(dt, dev);
+    void *csp = ptr(cs, dev), *op = ptr(&o, dev);
+    float* sp = ptr_as<float>(&state, dev);
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = p_layer_draft(&d, xp, xc, cwp, csp, cc, s.cu, s.slots, s.reset, s.accepted, s.n, T, ap, bp,
+                       alp, dtp, eps, q_scale, sp, &rec.c, op, oc, s.ws, s.ws_bytes, gp,
+                       where.stream);
+    Py_END_ALLOW_THREADS
+    return status(rc);
+  });
+}
+
+// bind(linear, draft_step, layer_draft, draft_workspace_size): addresses in the loaded library.
+PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  void* p[4];
+  for (int i = 0; i < 4; ++i) {
+    p[i] = n == 4 ? PyLong_AsVoidPtr(a[i]) : nullptr;
+    if (!p[i]) {
+      if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "gdn: bind takes 4 addresses");
+      return nullptr;
+    }
+  }
+  p_linear = reinterpret_cast<decltype(p_linear)>(p[0]);
+  p_draft_step = reinterpret_cast<decltype(p_draft_step)>(p[1]);
+  p_layer_draft = reinterpret_cast<decltype(p_layer_draft)>(p[2]);
+  p_draft_workspace = reinterpret_cast<decltype(p_draft_workspace)>(p[3]);
+  Py_RETURN_NONE;
+}
+
+#define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL
+PyMethodDef methods[] = {{"linear", FAST(linear), nullptr},
+                         {"draft_step", FAST(draft_step), nullptr},
+                         {"layer_draft", FAST(layer_draft), nullptr},
+                         {"bind", FAST(bind), nullptr},
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_fast", nullptr, -1, methods,
+                          nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__fast() {
+  const char* text[N_NAMES] = {"n_slots", "H_k", "H_v", "d_k", "d_v", "d_conv", "layout", "n", "e",
+                               "k", "u", "x", "z", "norm_w", "eps"};
+  for (int i = 0; i < N_NAMES; ++i)
+    if (!(names[i] = PyUnicode_InternFromString(text[i]))) return nullptr;
+  return PyModule_Create(&module_def);
+}

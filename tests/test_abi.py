@@ -306,3 +306,32 @@ def test_decode_pipe_host_validation(lib):
     assert lib.gdn_decode_pipe_step(None, A, A, A, A, None, A) == _lib.GDN_EINVAL
     assert lib.gdn_decode_pipe_flush(None) == _lib.GDN_EINVAL
     assert lib.gdn_decode_pipe_destroy(None) == _lib.GDN_OK
+
+
+def test_compiled_marshalling_refuses_on_the_host():
+    """_fast.so loads and turns away what is no CUDA tensor before it looks at the library."""
+    import torch
+
+    import gated_deltanet_linear_19_b200 as gdn
+    _build.build()
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        gdn.linear(x, x)
+    with pytest.raises(ValueError):
+        gdn.linear(x, None)
+    with pytest.raises(ValueError):
+        gdn.linear(x, "w")
+    with pytest.raises(ValueError):
+        gdn.linear(x[0], x)
+    dims, rec = gdn.Dims(2, 1, 1, 64, 64), gdn.draft_record(gdn.Dims(2, 1, 1, 64, 64), 4,
+                                                            device="cpu")
+    state, none = torch.zeros((2, 1, 64, 64)), torch.zeros((0, 1, 64))
+    gates = torch.zeros((0, 1))
+    slots = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        gdn.draft_step(dims, none, none, none, gates, gates, state, slots, None, None, rec, none)
+    with pytest.raises(ValueError):
+        gdn.layer_draft(dims, torch.zeros((0, 192)), None, None, None, slots, None, None, None,
+                        torch.zeros(1), torch.zeros(1), state, rec, none)
+    with pytest.raises(AttributeError):
+        gdn.draft_step(None, none, none, none, gates, gates, state, slots, None, None, rec, none)

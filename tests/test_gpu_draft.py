@@ -432,9 +432,19 @@ def test_python_refusals():
     for bad in (dict(slot_ids=ok["slot_ids"].long()), dict(cu_seqlens=cu_of([1, 1])),
                 dict(accepted=i32([0, 0])), dict(accepted=ok["accepted"].long()),
                 dict(record=gdn.draft_record(Dims(3, 1, 2, 64, 64), 4)),
-                dict(record=gdn.DraftRecord(rec.n, rec.e, rec.k, rec.u.double()))):
+                dict(record=gdn.DraftRecord(rec.n, rec.e, rec.k, rec.u.double())),
+                dict(workspace=torch.empty(1 << 20, dtype=torch.uint8))):
         with pytest.raises(ValueError):
             call(**bad)
+    args = dict(q=q, k=k, v=v, g=g, beta=beta, state=state, o=o)
+    for name, t in (("q", q[:, :, :32].contiguous()), ("k", k[:1]), ("k", k.half()), ("v", v[:1]),
+                    ("v", v.double()), ("g", g[:1]), ("g", g.half()), ("beta", beta.cpu()),
+                    ("state", state[:3]), ("state", state.half()), ("o", o[:1]), ("o", o.cpu()),
+                    ("q", q.transpose(0, 1)), ("o", None)):
+        w = {**args, name: t}
+        with pytest.raises(ValueError):
+            gdn.draft_step(dims, w["q"], w["k"], w["v"], w["g"], w["beta"], w["state"],
+                           ok["slot_ids"], ok["cu_seqlens"], None, rec, w["o"])
     with pytest.raises(gdn.GdnError) as e:
         call(workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
     assert e.value.status == gdn._lib.GDN_EWORKSPACE
@@ -596,3 +606,44 @@ def test_scales_of_state_and_keys():
         ref, bnd = m.draft(n, *(f64(t)[sl] for t in (q, k, v, g, beta)))
         near(f64(o)[sl], ref, bnd, 3, 128, f"o at {n}")
         near(f64(rec.u)[n, :, :3], m.u[n, :, :3], m.ub[n, :, :3], 3, 128, f"u at {n}")
+
+
+def test_layer_refusals():
+    dims = Dims(n_slots=2, H_k=1, H_v=2, d_k=64, d_v=64)
+    layer = GDNLayer(dims, torch.randn(dims.conv_dim, 4), torch.zeros(2), torch.zeros(2))
+    rec = layer.draft_record(3)
+    x, a, b = layer_inputs(dims, 2, torch.Generator().manual_seed(1), torch.bfloat16)
+    gate = OutGate(torch.zeros((2, 2, 64), device="cuda"), torch.ones(64, device="cuda"))
+
+    def call(x=x, a=a, b=b, rec=rec, gate=gate, cu=cu_of([2])):
+        layer.draft(x, a, b, cu, i32([0]), i32([0]), rec, gate=gate)
+
+    call()
+    for bad in (dict(x=x[:, :-4].contiguous()), dict(a=a[:1]), dict(b=b.half()),
+                dict(rec=gdn.DraftRecord(rec.n, rec.e, rec.k, rec.u)),
+                dict(rec=gdn.DraftRecord(rec.n, rec.e, rec.k, rec.u, rec.x.float())),
+                dict(gate=OutGate(gate.z[:1], gate.norm_w)),
+                dict(gate=OutGate(gate.z, gate.norm_w[:32])), dict(cu=cu_of([1, 1]))):
+        with pytest.raises(ValueError):
+            call(**bad)
+    assert device_status() == 0
+
+
+def test_a_stream_of_its_own_without_a_workspace():
+    """The workspace made for a call on another stream is that stream's: the current stream may
+    take memory and write it meanwhile."""
+    dims, gen, state, rec = small(n_slots=8, depth=5)
+    q, k, v, g, beta, o = inputs(dims, 8, gen, torch.float16)
+    slots, cu = i32([6, 2]), cu_of([5, 3])
+    want_o = torch.empty_like(o)
+    gdn.draft_step(dims, q, k, v, g, beta, state, slots, cu, None, rec, want_o)
+    want = rec.u.clone()
+    side = torch.cuda.Stream()
+    for _ in range(20):
+        rec.u.zero_()
+        side.wait_stream(torch.cuda.current_stream())
+        gdn.draft_step(dims, q, k, v, g, beta, state, slots, cu, None, rec, o, stream=side)
+        torch.full((gdn.draft_workspace_size(dims, 8, 2, 5),), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(o, want_o) and torch.equal(rec.u, want)
+    assert device_status() == 0
