@@ -43,6 +43,13 @@ struct LinearKernelArgs {
   int32_t* status;
 };
 
+// The matrix unit cuts off, it does not round, what lies below the accumulator's 24 bits, so a long
+// sum leaves an error of one sign that grows with K: 1.0e-6 of an fp32 output at K = 1024, 2.1e-6 at
+// 2048, 9.1e-6 at 8192. For fp32 outputs the accumulator is therefore changed every LN_KC elements
+// of K and the partial sums are added rounded: 2.5e-7 at any K. 16-bit outputs, rounded by 2^-9 and
+// 2^-12, do not see the cut.
+constexpr int LN_KC = 256;
+
 // ---------------------------------------------------------------- epilogue
 // The activation is a template argument of the kernels and the types are chosen once per 4 values,
 // so that the loop that runs is short: as one unrolled body of every variant, instruction fetch
@@ -253,18 +260,21 @@ constexpr int lt_epi(int bm) { return bm <= 16 ? 4 : 8; }
 // costs more than its loads in flight gain.
 constexpr int lt_rows(int bm) { return bm <= 16 ? 1 : bm <= 32 ? 2 : bm <= 64 ? 4 : 8; }
 
-template <int BM, int ACT>
+// CHUNKED: K in chunks of LN_KC, each in one of two accumulators in turn, added up in the epilogue
+// warps' registers.
+template <int BM, int ACT, bool CHUNKED>
 __global__ void __launch_bounds__(BM <= 16 ? 256 : ln_threads(lt_epi(BM)), BM <= 16 ? 2 : 1)
 linear_tile_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_constant__ CUtensorMap tm_w,
                    const __grid_constant__ CUtensorMap tm_x) {
   constexpr int NST = lt_stages(BM), SB = lt_stage(BM), SUB = lt_sub(BM), BK = 64 * SUB;
   constexpr uint32_t TCOLS = BM < 32 ? 32 : BM;
+  constexpr int GROUPS = BM / (lt_epi(BM) * 4);  // groups of 16 tokens that an epilogue warp sums
   constexpr int LN_EPI = lt_epi(BM), LN_TMA = LN_EPI, LN_MMA = LN_EPI + 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
   float* sums = reinterpret_cast<float*>(sm + NST * SB);  // [source rank][token][column]
-  __shared__ uint64_t full[NST], empty[NST], done, joined;
+  __shared__ uint64_t full[NST], empty[NST], tfull[2], tempty[2], joined;
   __shared__ uint32_t tmem_base;
   __shared__ int failed;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -275,6 +285,9 @@ linear_tile_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
   const int ksteps = (p.K + BK - 1) / BK;
   const int k0 = (int)((int64_t)ksteps * rank / split);
   const int nk = (int)((int64_t)ksteps * (rank + 1) / split) - k0;
+  // K steps of a chunk (LN_KC) and chunks; two accumulators take turns
+  const int run = CHUNKED && nk > LN_KC / BK ? LN_KC / BK : nk;
+  const int chunks = CHUNKED ? (nk + run - 1) / run : 1;
   // rank r finishes the tokens [r per, (r + 1) per) of the tile, of which cnt exist
   const int per = BM / split, per_log = 31 - __clz(per);
   const int64_t mr = m0 + (int64_t)rank * per;
@@ -282,14 +295,14 @@ linear_tile_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
 
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
-    mbar_init(&done, 1);
+    for (int i = 0; i < 2; ++i) { mbar_init(&tfull[i], 1); mbar_init(&tempty[i], LN_EPI); }
     mbar_init(&joined, 1);
     failed = 0;
     fence_mbar_init();
     if (split > 1) mbar_arrive_expect_tx(&joined, (uint32_t)(split * (cnt > 0 ? cnt : 0) * LN_BN * 4));
   }
   if (warp == LN_MMA) {
-    tmem_alloc(&tmem_base, TCOLS);
+    tmem_alloc(&tmem_base, (CHUNKED ? 2 : 1) * TCOLS);
     tmem_relinquish();  // at once: until then no other block is placed on this SM
   }
   fence_before_sync();
@@ -327,22 +340,30 @@ linear_tile_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
     __syncwarp();
   } else if (warp == LN_MMA) {
     if (elect_one()) {
-      for (int i = 0; i < nk; ++i) {
-        const int st = i % NST;
-        if (!mbar_wait(&full[st], (i / NST) & 1, &failed)) { failed = 1; break; }
-        fence_after_sync();
-        const uint32_t a = smem_u32(sm + st * SB);
-        const uint64_t da = desc_sw128(a, 16, 1024);
-        const uint64_t db = desc_sw128(a + SUB * LN_BN * 128, 16, 1024);
+      for (int c = 0, i = 0; c < chunks && !(CHUNKED && failed); ++c) {
+        const int buf = c & 1, end = (c + 1) * run < nk ? (c + 1) * run : nk;
+        if (CHUNKED && c >= 2) {
+          if (!mbar_wait(&tempty[buf], (c / 2 - 1) & 1, &failed)) { failed = 1; break; }
+          fence_after_sync();
+        }
+        const uint32_t d = tm + buf * TCOLS;
+        for (int first = i; i < (CHUNKED ? end : nk); ++i) {
+          const int st = i % NST;
+          if (!mbar_wait(&full[st], (i / NST) & 1, &failed)) { failed = 1; break; }
+          fence_after_sync();
+          const uint32_t a = smem_u32(sm + st * SB);
+          const uint64_t da = desc_sw128(a, 16, 1024);
+          const uint64_t db = desc_sw128(a + SUB * LN_BN * 128, 16, 1024);
 #pragma unroll
-        for (int u = 0; u < SUB; ++u)
+          for (int u = 0; u < SUB; ++u)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)  // 32 bytes along the swizzled row per K step
-            mma_f16(tm, da + u * (LN_BN * 8) + 2 * k, db + u * (BM * 8) + 2 * k, p.idesc,
-                    i > 0 || u > 0 || k > 0);
-        commit(&empty[st]);
+            for (int k = 0; k < 4; ++k)  // 32 bytes along the swizzled row per K step
+              mma_f16(CHUNKED ? d : tm, da + u * (LN_BN * 8) + 2 * k, db + u * (BM * 8) + 2 * k, p.idesc,
+                      i > (CHUNKED ? first : 0) || u > 0 || k > 0);
+          commit(&empty[st]);
+        }
+        commit(&tfull[buf]);
       }
-      commit(&done);
     }
     __syncwarp();
   }
@@ -358,30 +379,69 @@ linear_tile_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
     fetch_rows(p, res, mr, n0 + g, warp, LN_EPI, cnt);
   }
 
-  // the accumulator is complete
-  if (!mbar_wait(&done, 0, nullptr)) failed = 1;
-  fence_after_sync();
+  const int tokens = (int)(p.M - m0 < BM ? p.M - m0 : BM), col = (warp & 3) * 32 + lane;
+  const uint32_t mine = smem_u32(sums + rank * per * LN_BN + col), jbar = smem_u32(&joined);
+  // 16 tokens' partial sums to the rank that finishes them
+  auto send = [&](int c, const uint32_t (&r)[16]) {
+    if (split == 1) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sums[(c + i) * LN_BN + col] = __uint_as_float(r[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (c + i < tokens) {
+          const int to = (c + i) >> per_log, at = (c + i) & (per - 1);
+          st_async(at_rank(mine + (uint32_t)(at * LN_BN * 4), to), r[i], at_rank(jbar, to));
+        }
+    }
+  };
+  // the two warps of a lane quarter take alternating groups of 16 tokens
+  float acc[GROUPS][16];
+  if (CHUNKED && warp < LN_EPI) {
+#pragma unroll 1
+    for (int ch = 0; ch < chunks; ++ch) {
+      const int buf = ch & 1;
+      if (!mbar_wait(&tfull[buf], (ch / 2) & 1, &failed)) { failed = 1; break; }
+      fence_after_sync();
+#pragma unroll
+      for (int gr = 0; gr < GROUPS; ++gr) {
+        const int c = (warp >> 2) * 16 + gr * LN_EPI * 4;
+        if (c < tokens) {
+          uint32_t r[16];
+          tmem_ld16(taddr(tm, (warp & 3) * 32, buf * TCOLS + c), r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            acc[gr][i] = ch == 0 ? __uint_as_float(r[i]) : acc[gr][i] + __uint_as_float(r[i]);
+        }
+      }
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[buf]);
+    }
+  } else if (!CHUNKED) {
+    if (!mbar_wait(&tfull[0], 0, nullptr)) failed = 1;
+    fence_after_sync();
+  }
+  if (CHUNKED) __syncwarp();
   if (split > 1) cluster_wait();  // the other CTAs' barriers are ready
 
   if (warp < LN_EPI) {
-    // every token's partial sums to the rank that finishes it; the two warps of a lane quarter
-    // take alternating groups of 16 tokens
-    const int tokens = (int)(p.M - m0 < BM ? p.M - m0 : BM), col = (warp & 3) * 32 + lane;
-    const uint32_t mine = smem_u32(sums + rank * per * LN_BN + col), jbar = smem_u32(&joined);
-    for (int c = (warp >> 2) * 16; c < BM && c < tokens; c += LN_EPI * 4) {
-      uint32_t r[16];
-      tmem_ld16(taddr(tm, (warp & 3) * 32, c), r);
-      tmem_wait_ld();
-      if (split == 1) {
+    if (!CHUNKED) {
+      for (int c = (warp >> 2) * 16; c < BM && c < tokens; c += LN_EPI * 4) {
+        uint32_t r[16];
+        tmem_ld16(taddr(tm, (warp & 3) * 32, c), r);
+        tmem_wait_ld();
+        send(c, r);
+      }
+    } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sums[(c + i) * LN_BN + col] = __uint_as_float(r[i]);
-      } else {
+      for (int gr = 0; gr < GROUPS; ++gr) {
+        const int c = (warp >> 2) * 16 + gr * LN_EPI * 4;
+        uint32_t r[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (c + i < tokens) {
-            const int to = (c + i) >> per_log, at = (c + i) & (per - 1);
-            st_async(at_rank(mine + (uint32_t)(at * LN_BN * 4), to), r[i], at_rank(jbar, to));
-          }
+        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(acc[gr][i]);
+        if (c < tokens) send(c, r);
       }
     }
     if (split == 1)
@@ -415,7 +475,7 @@ linear_tile_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
   fence_before_sync();
   __syncthreads();
   if (failed && tid == 0) set_status(p.status, GDN_ETIMEOUT);
-  if (warp == LN_MMA) tmem_dealloc(tm, TCOLS);
+  if (warp == LN_MMA) tmem_dealloc(tm, (CHUNKED ? 2 : 1) * TCOLS);
 }
 
 // ---------------------------------------------------------------- pair kernel
@@ -426,13 +486,17 @@ linear_tile_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
 // into what L2 delivers (about 80 to 90 per SM, measured). Persistent: the pairs walk the tiles, the
 // two halves of tensor memory alternate as accumulators, and the epilogue of one tile runs under
 // the MMAs of the next.
-constexpr int LP_EPI = 8;
+// Chunked sums (LN_KC; here 512 elements, 5e-7, since a chunk has to last as long as the epilogue
+// needs to take it) live in the epilogue warps' registers: twice as many warps, of 64 columns each.
+constexpr int lp_epi(bool chunked) { return chunked ? 16 : 8; }
+constexpr int LP_KC = 512;
 constexpr int LP_T = 256;       // tokens and output columns of a tile
-constexpr int LP_STAGES = 6;
+constexpr int lp_stages(bool chunked) { return chunked ? 5 : 6; }
 constexpr int LP_HALF = 128 * 128;          // bytes of one operand's half tile of a stage
 constexpr int LP_STAGE = 2 * LP_HALF;       // this CTA's x and w rows
-constexpr int LP_OUT = LP_EPI * 32 * 128;   // per epilogue warp 32 rows x 32 fp32
-constexpr int LP_SMEM = LP_STAGES * LP_STAGE + LP_OUT + 1024;
+constexpr int lp_smem(bool chunked) {  // stages, and per epilogue warp 32 rows x 32 fp32
+  return lp_stages(chunked) * LP_STAGE + lp_epi(chunked) * 32 * 128 + 1024;
+}
 constexpr int LP_GROUP = 8;     // token tiles walked together, so that pairs share tiles in L2
 
 __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int x, int y,
@@ -472,11 +536,14 @@ __device__ __forceinline__ void tile_at(int64_t t, int64_t mt, int nt, int64_t* 
   *in = (int)(r / rows);
 }
 
-template <int ACT>
-__global__ void __launch_bounds__(ln_threads(LP_EPI), 1)
+// CHUNKED: K in chunks of LP_KC, each in an accumulator of its own turn (the two alternate over
+// chunks as they do over tiles).
+template <int ACT, bool CHUNKED>
+__global__ void __launch_bounds__(ln_threads(lp_epi(CHUNKED)), 1)
 linear_pair_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_constant__ CUtensorMap tm_w,
                    const __grid_constant__ CUtensorMap tm_x) {
-  constexpr int LN_EPI = LP_EPI, LN_TMA = LN_EPI, LN_MMA = LN_EPI + 1;
+  constexpr int LN_EPI = lp_epi(CHUNKED), LN_TMA = LN_EPI, LN_MMA = LN_EPI + 1;
+  constexpr int LP_STAGES = lp_stages(CHUNKED), COLS = 1024 / LN_EPI;  // columns of a warp
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
@@ -543,27 +610,32 @@ linear_pair_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
       int st = 0, buf = 0;
       uint32_t ph = 0, tph = 1;
       for (int64_t t = pair; t < tiles && !failed; t += pairs) {
-        if (!mbar_wait(&tempty[buf], tph, &failed)) { failed = 1; break; }
-        fence_after_sync();
-        const uint32_t d = tm + buf * LP_T;
-        for (int k = 0; k < ksteps; ++k) {
-          if (!mbar_wait(&full[st], ph, &failed)) { failed = 1; break; }
+        const int chunk = CHUNKED ? LP_KC / 64 : ksteps;
+        for (int kc = 0; kc < ksteps && !failed; kc += chunk) {
+          if (!mbar_wait(&tempty[buf], tph, &failed)) { failed = 1; break; }
           fence_after_sync();
-          const uint32_t a = smem_u32(sm + st * LP_STAGE);
-          const uint64_t da = desc_sw128(a, 16, 1024), db = desc_sw128(a + LP_HALF, 16, 1024);
+          const uint32_t d = tm + buf * LP_T;
+          const int end = kc + chunk < ksteps ? kc + chunk : ksteps;
+          for (int k = kc; k < end; ++k) {
+            if (!mbar_wait(&full[st], ph, &failed)) { failed = 1; break; }
+            fence_after_sync();
+            const uint32_t a = smem_u32(sm + st * LP_STAGE);
+            const uint64_t da = desc_sw128(a, 16, 1024), db = desc_sw128(a + LP_HALF, 16, 1024);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) mma_pair(d, da + 2 * q, db + 2 * q, p.idesc, k > 0 || q > 0);
-          commit_pair(&empty[st]);
-          if (++st == LP_STAGES) { st = 0; ph ^= 1; }
+            for (int q = 0; q < 4; ++q)
+              mma_pair(d, da + 2 * q, db + 2 * q, p.idesc, k > kc || q > 0);
+            commit_pair(&empty[st]);
+            if (++st == LP_STAGES) { st = 0; ph ^= 1; }
+          }
+          commit_pair(&tfull[buf]);
+          if (++buf == 2) { buf = 0; tph ^= 1; }
         }
-        commit_pair(&tfull[buf]);
-        if (++buf == 2) { buf = 0; tph ^= 1; }
       }
     }
     __syncwarp();
   } else {
     float* stage = reinterpret_cast<float*>(sm + LP_STAGES * LP_STAGE) + warp * 32 * 32;
-    const int quarter = (warp & 3) * 32, c0 = (warp >> 2) * 128;  // TMEM lanes, columns of the warp
+    const int quarter = (warp & 3) * 32, c0 = (warp >> 2) * COLS;  // TMEM lanes, columns of the warp
     const int q4 = lane & 7;
     int buf = 0;
     uint32_t ph = 0;
@@ -574,44 +646,89 @@ linear_pair_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
       const int64_t m = im * LP_T + rank * 128 + quarter;
       const int n0 = in * LP_T;
       const int cnt = m >= p.M ? 0 : p.M - m < 32 ? (int)(p.M - m) : 32;
-      if (!mbar_wait(&tfull[buf], ph, &failed)) { failed = 1; break; }
-      fence_after_sync();
+      // this warp has read its part of accumulator `buf`
+      auto release = [&]() {
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(at_rank(smem_u32(&tempty[buf]), 0));
+        if (++buf == 2) { buf = 0; ph ^= 1; }
+      };
+      float sum[CHUNKED ? COLS / 32 : 1][32];
+      if constexpr (CHUNKED) {
+#pragma unroll
+        for (int b = 0; b < COLS / 32; ++b)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[b][j] = 0.f;
 #pragma unroll 1
-      for (int c = c0; c < c0 + 128 && n0 + c < p.N && cnt > 0; c += 32) {
+        for (int kc = 0; kc < ksteps; kc += LP_KC / 64) {
+          if (!mbar_wait(&tfull[buf], ph, &failed)) { failed = 1; break; }
+          fence_after_sync();
+#pragma unroll
+          for (int b = 0; b < COLS / 16; ++b) {
+            uint32_t r[16];
+            tmem_ld16(taddr(tm, quarter, buf * LP_T + c0 + 16 * b), r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[b / 2][b % 2 * 16 + j] += __uint_as_float(r[j]);
+          }
+          release();
+        }
+        if (failed) break;
+      } else {
+        if (!mbar_wait(&tfull[buf], ph, &failed)) { failed = 1; break; }
+        fence_after_sync();
+      }
+#pragma unroll 1
+      for (int c = c0; c < c0 + COLS && n0 + c < p.N && cnt > 0; c += 32) {
         const int n = n0 + c + q4 * 4;
         const bool vec = p.vec && n0 + c + 32 <= p.N;
-        ResBatch<8> res;
+        constexpr int V = CHUNKED ? 2 : 8;  // rows per batch: what the sums leave of the registers
+        ResBatch<V> res;
         float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
         if (vec) {
           bias = bias_at(p, n);
           fetch_rows(p, res, m, n, lane >> 3, 4, cnt);
         }
-        uint32_t r[32];
-        tmem_ld32(taddr(tm, quarter, buf * LP_T + c), r);
-        tmem_wait_ld();
-        __syncwarp();  // the previous 32 columns have been read
         // row = lane; 16-byte groups swizzled by the row, so that rows written by a quarter-warp
         // and groups read by one both cover all banks
+        auto put = [&](const float* v) {
+          __syncwarp();  // the previous 32 columns have been read
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<float4*>(stage + lane * 32 + ((j ^ (lane & 7)) << 2)) =
-              make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
-                          __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<float4*>(stage + lane * 32 + ((j ^ (lane & 7)) << 2)) =
+                make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        };
+        if constexpr (CHUNKED) {
+#pragma unroll
+          for (int b = 0; b < COLS / 32; ++b)
+            if (c == c0 + 32 * b) put(sum[b]);
+        } else {
+          uint32_t r[32];
+          tmem_ld32(taddr(tm, quarter, buf * LP_T + c), r);
+          tmem_wait_ld();
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+          put(v);
+        }
         __syncwarp();
-        if (vec)
-          finish_rows<ACT, 8>(p, res, m, n, lane >> 3, 4, cnt, bias, [&](int row) {
-            return *reinterpret_cast<const float4*>(stage + row * 32 + ((q4 ^ (row & 7)) << 2));
-          });
+        auto staged = [&](int row) {
+          return *reinterpret_cast<const float4*>(stage + row * 32 + ((q4 ^ (row & 7)) << 2));
+        };
+        if (vec && !CHUNKED)
+          finish_rows<ACT, V>(p, res, m, n, lane >> 3, 4, cnt, bias, staged);
+        else if (vec)
+#pragma unroll 1
+          for (int r0 = lane >> 3; r0 < cnt; r0 += 4 * V) {
+            if (r0 != (lane >> 3)) fetch_rows(p, res, m, n, r0, 4, cnt);
+            finish_rows<ACT, V>(p, res, m, n, r0, 4, cnt, bias, staged);
+          }
         else
-          finish_column<ACT, 16>(p, m, n0 + c + lane, 0, 1, cnt, [&](int row) {
+          finish_column<ACT, 2 * V>(p, m, n0 + c + lane, 0, 1, cnt, [&](int row) {
             return stage[row * 32 + (((lane >> 2) ^ (row & 7)) << 2) + (lane & 3)];
           });
       }
-      // this warp has read its part of the accumulator
-      fence_before_sync();
-      __syncwarp();
-      if (lane == 0) arrive_cluster(at_rank(smem_u32(&tempty[buf]), 0));
-      if (++buf == 2) { buf = 0; ph ^= 1; }
+      if constexpr (!CHUNKED) release();
     }
     __syncwarp();
   }
@@ -658,15 +775,15 @@ LinearKernelArgs kernel_args(const LinearArgs& a) {
   return k;
 }
 
-template <int BM, int ACT>
-cudaError_t launch_tile(const LinearArgs& a, int sms, cudaStream_t s) {
+template <int BM, int ACT, bool CHUNKED>
+cudaError_t launch_tile_as(const LinearArgs& a, int sms, cudaStream_t s) {
   const bool bf16 = a.dtype == GDN_BF16;
   static std::atomic<int> smem_set[64];
   alignas(64) CUtensorMap tm_w, tm_x;
   cudaError_t e = make_map(&tm_w, a.w, bf16, a.N, a.K, a.ldw, LN_BN);
   if (e == cudaSuccess) e = make_map(&tm_x, a.x, bf16, a.M, a.K, a.ldx, BM);
   if (e == cudaSuccess)
-    e = allow_smem(linear_tile_kernel<BM, ACT>, lt_smem(BM), smem_set);
+    e = allow_smem(linear_tile_kernel<BM, ACT, CHUNKED>, lt_smem(BM), smem_set);
   if (e != cudaSuccess) return e;
   const int64_t nt = (a.N + LN_BN - 1) / LN_BN, mt = (a.M + BM - 1) / BM;
   if (mt > 65535) return cudaErrorInvalidValue;
@@ -691,10 +808,16 @@ cudaError_t launch_tile(const LinearArgs& a, int sms, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, linear_tile_kernel<BM, ACT>, k, tm_w, tm_x);
+  return cudaLaunchKernelEx(&cfg, linear_tile_kernel<BM, ACT, CHUNKED>, k, tm_w, tm_x);
 }
 
-template <int ACT>
+template <int BM, int ACT>
+cudaError_t launch_tile(const LinearArgs& a, int sms, cudaStream_t s) {
+  return a.out_dtype == GDN_F32 && a.K > LN_KC ? launch_tile_as<BM, ACT, true>(a, sms, s)
+                                               : launch_tile_as<BM, ACT, false>(a, sms, s);
+}
+
+template <int ACT, bool CHUNKED>
 cudaError_t launch_pair(const LinearArgs& a, int sms, cudaStream_t s) {
   const bool bf16 = a.dtype == GDN_BF16;
   static std::atomic<int> smem_set[64];
@@ -702,7 +825,7 @@ cudaError_t launch_pair(const LinearArgs& a, int sms, cudaStream_t s) {
   cudaError_t e = make_map(&tm_w, a.w, bf16, a.N, a.K, a.ldw, 128);
   if (e == cudaSuccess) e = make_map(&tm_x, a.x, bf16, a.M, a.K, a.ldx, 128);
   if (e == cudaSuccess)
-    e = allow_smem(linear_pair_kernel<ACT>, LP_SMEM, smem_set);
+    e = allow_smem(linear_pair_kernel<ACT, CHUNKED>, lp_smem(CHUNKED), smem_set);
   if (e != cudaSuccess) return e;
   const int64_t tiles = ((a.M + LP_T - 1) / LP_T) * ((a.N + LP_T - 1) / LP_T);
   const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
@@ -717,12 +840,12 @@ cudaError_t launch_pair(const LinearArgs& a, int sms, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * pairs));
-  cfg.blockDim = dim3(ln_threads(LP_EPI));
-  cfg.dynamicSmemBytes = LP_SMEM;
+  cfg.blockDim = dim3(ln_threads(lp_epi(CHUNKED)));
+  cfg.dynamicSmemBytes = lp_smem(CHUNKED);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, linear_pair_kernel<ACT>, k, tm_w, tm_x);
+  return cudaLaunchKernelEx(&cfg, linear_pair_kernel<ACT, CHUNKED>, k, tm_w, tm_x);
 }
 
 template <int ACT>
@@ -732,7 +855,8 @@ cudaError_t launch_act(const LinearArgs& a, int sms, cudaStream_t s) {
   if (a.M <= 64) return launch_tile<64, ACT>(a, sms, s);
   const int64_t t128 = ((a.M + 127) / 128) * ((a.N + 127) / 128);
   if (t128 <= sms) return launch_tile<128, ACT>(a, sms, s);
-  return launch_pair<ACT>(a, sms, s);
+  if (a.out_dtype == GDN_F32 && a.K > LP_KC) return launch_pair<ACT, true>(a, sms, s);
+  return launch_pair<ACT, false>(a, sms, s);
 }
 
 }  // namespace

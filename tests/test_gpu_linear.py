@@ -134,6 +134,27 @@ def test_same_bits_every_time_and_alone_or_in_a_batch():
     assert torch.equal(linear(x[3:4], w, out_dtype=torch.float32), y[3:4])
 
 
+@pytest.mark.parametrize("m,n", [(1, 2048), (1, 12288), (50, 20000), (100, 12288), (200, 4096),
+                                 (900, 5003), (2048, 2048)])
+def test_long_sums_keep_fp32(m, n):
+    """The matrix unit cuts its running sum off, so one accumulator's relative error grows with K in
+    proportion. Partial sums of 256 elements, added rounded, do not: each keeps the relative error
+    that it has alone, so the whole has that of K = 256, a quarter more for the draw of the inputs,
+    and roundings: log2 of the partial sums' number, each by 2^-24 at most in the L2 norm of values
+    whose running sum stays below the final one's size, 8 of them for K up to 65536."""
+    def error(k):
+        gen = torch.Generator().manual_seed(k)
+        x, w = rows(m, k, gen, torch.bfloat16), rows(n, k, gen, torch.bfloat16, scale=k ** -0.5)
+        ref = reference(x, w)[0]
+        return float((linear(x, w, out_dtype=torch.float32).double() - ref).norm() / ref.norm())
+
+    short = max(error(256), error(512))
+    for k in (1024, 2048, 4104, 8192):
+        e = error(k)
+        assert e <= 1.25 * short + 8 * 2.0 ** -24, f"K = {k}: {e:.2e}, K = 256: {short:.2e}"
+    assert device_status() == 0
+
+
 def test_streams_graph_and_chains():
     """Chained products (each reading what the one before wrote), eager, on a side stream and
     replayed from a graph."""
