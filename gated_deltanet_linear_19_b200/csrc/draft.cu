@@ -838,10 +838,13 @@ __global__ void __launch_bounds__(DR_THREADS, st_blocks(MAXT))
 #pragma unroll
             for (int j4 = 0; 4 * j4 < N && 4 * j4 <= r * TEAMS + TEAMS - 1; ++j4) {
               const float4 c = *reinterpret_cast<const float4*>(cP + i * N + 4 * j4);
-              o = fmaf(c.x, u[4 * j4], o);
-              o = fmaf(c.y, u[4 * j4 + 1], o);
-              o = fmaf(c.z, u[4 * j4 + 2], o);
-              o = fmaf(c.w, u[4 * j4 + 3], o);
+              const float cj[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                // tokens behind this one stay out altogether: theirs may be infinite or NaN
+                const int m = 4 * j4 + b - r * TEAMS;
+                if (m <= 0 || (m < TEAMS && m <= team)) o = fmaf(cj[b], u[4 * j4 + b], o);
+              }
             }
             if (p.o_dtype == GDN_F32) static_cast<float*>(p.o)[o0 + i * tok] = o;
             else st(static_cast<__nv_bfloat16*>(p.o) + o0 + i * tok, o);

@@ -647,3 +647,34 @@ def test_a_stream_of_its_own_without_a_workspace():
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(o, want_o) and torch.equal(rec.u, want)
     assert device_status() == 0
+
+
+@pytest.mark.parametrize("depth", [4, 8, 16])
+def test_nan_and_infinity_stay_behind_their_token(depth):
+    """A token that is not finite leaves the tokens before it, the other sequences and the
+    committed state as they were; committing only what lies before it is clean."""
+    dims = Dims(n_slots=3, H_k=1, H_v=2, d_k=64, d_v=64)
+    gen = torch.Generator().manual_seed(depth)
+    state = torch.randn((3, 2, 64, 64), generator=gen).cuda()
+    rec = gdn.draft_record(dims, depth)
+    q, k, v, g, beta, o = inputs(dims, 2 * depth, gen, torch.float32)
+    args = (i32([0, 2]), cu_of([depth, depth]))
+    s0, r0 = state.clone(), gdn.draft_record(dims, depth)
+    want = torch.empty_like(o)
+    gdn.draft_step(dims, q, k, v, g, beta, s0, *args, None, r0, want)
+    for at in range(1, depth):
+        for t, value in ((k, float("nan")), (v, float("inf")), (q, float("nan"))):
+            bad = t.clone()
+            bad[at] = value
+            x = {id(q): q, id(k): k, id(v): v}
+            x[id(t)] = bad
+            gdn.draft_step(dims, x[id(q)], x[id(k)], x[id(v)], g, beta, state, *args, None, rec, o)
+            assert torch.equal(o[:at], want[:at]) and torch.equal(o[depth:], want[depth:])
+            assert not torch.isfinite(o[at]).all()
+            assert torch.equal(rec.u[0, :, :at], r0.u[0, :, :at]) and torch.equal(rec.u[2], r0.u[2])
+            assert torch.equal(state, s0)
+    none = [t[:0] for t in (q, k, v, g, beta)]
+    for st, r in ((state, rec), (s0, r0)):
+        gdn.draft_step(dims, *none, st, i32([0, 2]), cu_of([0, 0]), i32([depth - 1, depth]), r,
+                       o[:0].clone())
+    assert torch.equal(state, s0) and device_status() == 0
