@@ -589,8 +589,6 @@ __global__ void __launch_bounds__(DR_THREADS, st_blocks(MAXT))
     }
   };
 
-  // ---- the first tile's state, before the first kernel's decision on its sequence is known (the
-  // state was written before that kernel started)
   // Word `lane` of tile t (warp 0, lanes 0..11); zeros, nothing to do, for t >= total.
   auto tile_word = [&](unsigned t) {
     const unsigned n = t / per, rem = t - n * per;
@@ -599,8 +597,8 @@ __global__ void __launch_bounds__(DR_THREADS, st_blocks(MAXT))
     return lane == 8 ? (int)n : lane == 9 ? (int)(rem / TILES) : lane == 10 ? (int)(rem % TILES) : 0;
   };
   // From the third on, tiles are taken in order by whichever block is free (drafts differ in
-  // length). Warp 0 is two tiles ahead: `t1` is the number of the next tile, `ahead` a word of it, `t2` the number of the
-  // one after, each asked for a tile before it is used.
+  // length). Warp 0 is two tiles ahead: `t1` is the number of the next tile, `ahead` a word of it,
+  // `t2` the number of the one after, each asked for a tile before it is used.
   unsigned* next = reinterpret_cast<unsigned*>(const_cast<uint8_t*>(ws) + p.ws_next);
   auto take = [&]() {
     unsigned t = 0;
@@ -609,6 +607,8 @@ __global__ void __launch_bounds__(DR_THREADS, st_blocks(MAXT))
   };
   unsigned t1 = total, t2 = total;
   int ahead = 0;
+  // ---- the first tile's state, before the first kernel's decision on its sequence is known (the
+  // state was written before that kernel started)
   bool early = false;
   {
     const unsigned n = blockIdx.x / per, rem = blockIdx.x - n * per;

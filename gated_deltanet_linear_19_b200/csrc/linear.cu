@@ -682,7 +682,9 @@ linear_pair_kernel(const __grid_constant__ LinearKernelArgs p, const __grid_cons
       for (int c = c0; c < c0 + COLS && n0 + c < p.N && cnt > 0; c += 32) {
         const int n = n0 + c + q4 * 4;
         const bool vec = p.vec && n0 + c + 32 <= p.N;
-        constexpr int V = CHUNKED ? 2 : 8;  // rows per batch: what the sums leave of the registers
+        // rows per batch: what the sums leave of the registers (4096 tokens to 8192 columns in fp32:
+        // 146 us with 4 rows, 126 with 2, 117 with 1)
+        constexpr int V = CHUNKED ? 1 : 8;
         ResBatch<V> res;
         float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
         if (vec) {
